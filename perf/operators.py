@@ -1,0 +1,351 @@
+"""Cases of the expert operators and the 4-bit base products, for timing and for comparing their outputs.
+
+The operators: the base output of a projection from 4-bit weights with a scale (and a zero point) per
+group, y = W x (`base`), the same with one matrix per expert over rows sorted by expert (`experts`),
+and the sort of a batch's tokens by expert with the way back: order and gather (`dispatch`), weighted
+sum (`combine`), the gradients of both (`train`), and an expert projection from router to sum (`step`).
+
+Where `own` is false, `run` computes each in elementary torch operations in 32 bits; where it is true
+it makes the library's calls.  `exact` is the definition in 64 bits.
+"""
+from __future__ import annotations
+
+import torch
+
+own = False
+
+BF16, F32 = "bf16", "fp32"
+_DT = {BF16: torch.bfloat16, F32: torch.float32}
+
+
+# ----------------------------------------------------------------------------
+# cases
+# ----------------------------------------------------------------------------
+
+def _base(name, T, d_in, d_out, group, zeros, scales, y):
+    return dict(name=name, op="base", T=T, d_in=d_in, d_out=d_out, group=group, zeros=zeros, scales=scales, y=y)
+
+
+def _experts(name, op, T, k, E, d_in, d_out, group, zeros, scales, y):
+    return dict(name=name, op=op, T=T, k=k, E=E, d_in=d_in, d_out=d_out, group=group, zeros=zeros, scales=scales, y=y)
+
+
+def _rows(name, op, T, k, E, d, ys, y, drop):
+    return dict(name=name, op=op, T=T, k=k, E=E, d=d, ys=ys, y=y, drop=drop)
+
+
+def listed():
+    return [
+        # one sequence's decode step through a 70B-shaped q projection
+        _base("base_q_1", 1, 8192, 8192, 128, False, BF16, BF16),
+        # three sequences through the k projection: few output rows, a finer group, zero points, strict y
+        _base("base_k_3", 3, 8192, 1024, 64, True, BF16, F32),
+        # the decode batch of 32 requests through the down projection: the longest rows
+        _base("base_down_32", 32, 28672, 8192, 128, True, BF16, BF16),
+        # a mid-size batch through an MLP up projection, the finest group, fp32 scales, strict y
+        _base("base_up_256", 256, 4096, 14336, 32, False, F32, F32),
+        # prefill of 8 requests x 512 tokens through a 70B-shaped projection
+        _base("base_prefill_4096", 4096, 8192, 8192, 128, False, BF16, BF16),
+        # expert projections of a decode batch: most experts have a row or two, rows gathered by the product
+        _experts("experts_decode_32", "experts", 32, 4, 64, 4096, 1536, 128, True, BF16, BF16),
+        # expert projections of a prefill batch: hundreds of rows an expert
+        _experts("experts_prefill_2048", "experts", 2048, 4, 32, 4096, 4096, 128, False, BF16, BF16),
+        # a decode step from the router's choice to the weighted sum added to the residual
+        _experts("step_decode_17", "step", 17, 2, 16, 2048, 2048, 64, False, BF16, BF16),
+        # a decode batch's tokens to their experts' rows
+        _rows("dispatch_decode_32", "dispatch", 32, 4, 64, 8192, BF16, BF16, 0.0),
+        # a prefill batch's tokens to their experts' rows, some dropped at the experts' capacity
+        _rows("dispatch_prefill_8192", "dispatch", 8192, 4, 128, 4096, BF16, BF16, 0.05),
+        # the way back: fp32 expert rows, weighted, added to a bf16 residual of odd width
+        _rows("combine_1001", "combine", 1001, 4, 64, 4097, F32, BF16, 0.05),
+        # a training step's gradients of the gather and of the weighted sum
+        _rows("train_4096", "train", 4096, 4, 64, 8192, BF16, BF16, 0.02),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(lo * (hi / lo) ** rng.random()))
+
+
+def draw(rng):
+    op = rng.choice(["base", "base", "base", "experts", "experts", "step", "dispatch", "combine", "train"])
+    if op in ("base", "experts", "step"):
+        group = rng.choice([32, 64, 128])
+        zeros, scales, y = rng.random() < 0.5, rng.choice([BF16, F32]), rng.choice([BF16, F32])
+        if op == "base":
+            d_in, d_out = group * max(1, _log(rng, 512, 28672) // group), _log(rng, 128, 28672)
+            most = min(4096, (1 << 38) // (d_in * d_out))  # no more products than the largest listed case
+            return dict(op=op, T=_log(rng, 1, max(2, most)), d_in=d_in, d_out=d_out, group=group, zeros=zeros, scales=scales, y=y)
+        E = _log(rng, 2, 64)
+        d_in, d_out = group * max(1, _log(rng, 512, 6144) // group), _log(rng, 256, 4096)
+        k = rng.randint(1, min(8, E))
+        T = _log(rng, 1, min(64 if op == "step" else 2048, 16384 // k))
+        return dict(op=op, T=T, k=k, E=E, d_in=d_in, d_out=d_out, group=group, zeros=zeros, scales=scales, y=y)
+    E = _log(rng, 2, 512)
+    k, d = rng.randint(1, min(8, E)), _log(rng, 128, 8192)
+    T = _log(rng, 1, min(16384, 33554432 * 4 // (k * d)))
+    ys = rng.choice([BF16, F32])
+    return dict(op=op, T=T, k=k, E=E, d=d, ys=ys, y=rng.choice([BF16, F32]) if op == "combine" else ys, drop=rng.choice([0.0, 0.05, 0.3]))
+
+
+# ----------------------------------------------------------------------------
+# inputs
+# ----------------------------------------------------------------------------
+
+def _randn(g, *shape, dtype=BF16, std=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(_DT[dtype])
+
+
+def _choice(g, T, k, E, drop, skew):
+    """A router's choice: k distinct experts a token; `skew`: some experts are liked better; some slots dropped (-1)."""
+    score = torch.rand(T, E, generator=g, device="cuda")
+    if skew:
+        score = score * (0.5 + torch.rand(E, generator=g, device="cuda"))
+    ids = score.topk(k, dim=1).indices.to(torch.int32)
+    if drop:
+        ids = torch.where(torch.rand(T, k, generator=g, device="cuda") < drop, -1, ids)
+    return ids
+
+
+def _shares(g, T, k):
+    """The router's weights: positive, a token's sum to one."""
+    return torch.softmax(torch.randn(T, k, generator=g, device="cuda"), dim=1)
+
+
+def _order(ids, E):
+    """(offsets, row_of, slot_of) of the stable sort of the slots by expert."""
+    flat = ids.reshape(-1).long()
+    key = torch.where(flat < 0, E, flat)
+    slot = torch.argsort(key, stable=True)
+    counts = torch.bincount(key, minlength=E + 1)[:E]
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)])
+    row = torch.empty_like(slot)
+    row[slot] = torch.arange(slot.numel(), device=slot.device)
+    row_of = torch.where(flat < 0, -1, row)
+    slot_of = torch.where(torch.arange(slot.numel(), device=slot.device) < offsets[E], slot, -1)
+    return offsets.int(), row_of.reshape(ids.shape).int(), slot_of.int()
+
+
+def prepare(case, seed):
+    c = case
+    g = torch.Generator(device="cuda").manual_seed(int(seed) * 1000003 + 17)
+    op, T = c["op"], c["T"]
+    s = dict(op=op, c=c)
+    if op in ("base", "experts", "step"):
+        lead = () if op == "base" else (c["E"],)
+        d_in, d_out, n_groups = c["d_in"], c["d_out"], c["d_in"] // c["group"]
+        s["codes"] = torch.randint(0, 256, (*lead, d_out, d_in // 2), generator=g, device="cuda", dtype=torch.uint8)
+        s["scales"] = ((0.5 + torch.rand(*lead, d_out, n_groups, generator=g, device="cuda")) * (0.2 / d_in ** 0.5)).to(_DT[c["scales"]])
+        s["zeros"] = torch.randint(5, 12, (*lead, d_out, n_groups), generator=g, device="cuda", dtype=torch.uint8) if c["zeros"] else None
+        s["x"] = _randn(g, T, d_in)
+        rows = T
+        if op != "base":
+            rows = T * c["k"]
+            ids = _choice(g, T, c["k"], c["E"], 0.0, False)
+            if op == "experts":
+                s["offsets"], s["row_of"], s["slot_of"] = _order(ids, c["E"])
+            else:
+                s.update(ids=ids, weights=_shares(g, T, c["k"]), offsets=torch.empty(c["E"] + 1, dtype=torch.int32, device="cuda"), row_of=torch.empty_like(ids),
+                         slot_of=torch.empty(rows, dtype=torch.int32, device="cuda"), out=torch.empty(T, d_out, dtype=_DT[c["y"]], device="cuda"))
+            s["cap"] = int(torch.bincount(ids.reshape(-1).long(), minlength=c["E"]).max())  # rows of the fullest expert
+        s["y"] = torch.empty(rows, d_out, dtype=_DT[c["y"]], device="cuda")
+        return s
+    k, E, d = c["k"], c["E"], c["d"]
+    ids = _choice(g, T, k, E, c["drop"], True)
+    if op == "dispatch":
+        s.update(ids=ids, x=_randn(g, T, d, dtype=c["ys"]), offsets=torch.empty(E + 1, dtype=torch.int32, device="cuda"), row_of=torch.empty_like(ids),
+                 slot_of=torch.empty(T * k, dtype=torch.int32, device="cuda"), xs=torch.zeros(T * k, d, dtype=_DT[c["ys"]], device="cuda"))
+        return s
+    s["offsets"], s["row_of"], s["slot_of"] = _order(ids, E)
+    s["weights"] = _shares(g, T, k)
+    s["ys"] = _randn(g, T * k, d, dtype=c["ys"])
+    if op == "combine":
+        s["residual"] = _randn(g, T, d, dtype=c["y"])
+        s["y"] = torch.empty_like(s["residual"])
+    else:
+        s["dy"] = _randn(g, T, d, dtype=c["y"])
+        s["dxs"] = _randn(g, T * k, d, dtype=c["ys"])
+        s["dys"] = torch.zeros(T * k, d, dtype=_DT[c["ys"]], device="cuda")
+        s["dweights"] = torch.empty(T, k, device="cuda")
+        s["dx"] = torch.empty(T, d, dtype=_DT[c["ys"]], device="cuda")
+    return s
+
+
+# ----------------------------------------------------------------------------
+# one pass
+# ----------------------------------------------------------------------------
+
+def run(state):
+    if own:
+        return _calls(state)
+    return _plain(state)
+
+
+def _calls(s):
+    import segmented_rank_gemm_sgmv_b200 as sg
+    op = s["op"]
+    if op == "base":
+        sg.base_product(s["x"], s["codes"], s["scales"], s["y"], zeros=s["zeros"])
+        return s["y"]
+    if op == "experts":
+        sg.base_product_experts(s["x"], s["codes"], s["scales"], s["offsets"], s["y"], zeros=s["zeros"], slot_of=s["slot_of"])
+        return s["y"]
+    if op == "step":
+        sg.expert_order(s["ids"], s["c"]["E"], s["offsets"], s["row_of"], s["slot_of"])
+        sg.base_product_experts(s["x"], s["codes"], s["scales"], s["offsets"], s["y"], zeros=s["zeros"], slot_of=s["slot_of"])
+        sg.expert_combine(s["y"], s["row_of"], s["out"], weights=s["weights"])
+        return s["out"]
+    if op == "dispatch":
+        sg.expert_order(s["ids"], s["c"]["E"], s["offsets"], s["row_of"], s["slot_of"])
+        sg.expert_gather(s["x"], s["row_of"], s["xs"])
+        return s["offsets"], s["row_of"], s["slot_of"], s["xs"]
+    if op == "combine":
+        sg.expert_combine(s["ys"], s["row_of"], s["y"], weights=s["weights"], add=s["residual"])
+        return s["y"]
+    sg.expert_combine_backward(s["dy"], s["ys"], s["row_of"], s["weights"], s["dys"], s["dweights"])
+    sg.expert_gather_backward(s["dxs"], s["row_of"], s["dx"])
+    return s["dys"], s["dweights"], s["dx"]
+
+
+def _dense(s):
+    """The weights in 32 bits: (code - zero) * scale, [.., d_out, d_in]."""
+    n = torch.stack([s["codes"] & 15, s["codes"] >> 4], dim=-1).flatten(-2)
+    n = n.unflatten(-1, (-1, s["c"]["group"])).float()
+    if s["zeros"] is None:
+        n = n - 16 * (n >= 8)
+    else:
+        n = n - s["zeros"].float()[..., None]
+    return (n * s["scales"].float()[..., None]).flatten(-2)
+
+
+def _by_expert(s, offsets, slot_of):
+    """The expert products of sorted rows: the rows of each expert side by side, padded to the fullest one's, in one batched product."""
+    E, rows = s["c"]["E"], torch.arange(slot_of.numel(), device=slot_of.device)
+    expert = (rows[:, None] >= offsets[None, 1:]).sum(1)
+    place = rows - offsets.long()[expert]
+    x = s["x"].float()[slot_of.long() // s["c"]["k"]]
+    padded = x.new_zeros(E, s["cap"], x.shape[1])
+    padded[expert, place] = x
+    return torch.bmm(padded, _dense(s).transpose(1, 2))[expert, place]
+
+
+def _sum_back(ys, row_of, weights):
+    picked = ys.float()[row_of.long().clamp(min=0)] * (row_of >= 0)[..., None]
+    return (picked if weights is None else picked * weights[..., None]).sum(1)
+
+
+def _plain(s):
+    op, c = s["op"], s["c"]
+    if op == "base":
+        return (s["x"].float() @ _dense(s).T).to(_DT[c["y"]])
+    if op == "experts":
+        return _by_expert(s, s["offsets"], s["slot_of"]).to(_DT[c["y"]])
+    if op == "step":
+        offsets, row_of, slot_of = _order(s["ids"], c["E"])
+        return _sum_back(_by_expert(s, offsets, slot_of), row_of, s["weights"]).to(_DT[c["y"]])
+    if op == "dispatch":
+        offsets, row_of, slot_of = _order(s["ids"], c["E"])
+        xs = torch.where(slot_of[:, None] >= 0, s["x"][slot_of.long().clamp(min=0) // c["k"]], 0)
+        return offsets, row_of, slot_of, xs
+    if op == "combine":
+        return (s["residual"].float() + _sum_back(s["ys"], s["row_of"], s["weights"])).to(_DT[c["y"]])
+    row, kept = s["row_of"].long().clamp(min=0), s["row_of"] >= 0
+    dy = s["dy"].float()
+    dweights = (s["ys"].float()[row] * dy[:, None, :]).sum(2) * kept
+    slot = s["slot_of"].long().clamp(min=0)
+    dys = torch.where(s["slot_of"][:, None] >= 0, s["weights"].reshape(-1)[slot][:, None] * dy[slot // c["k"]], 0)
+    return dys.to(_DT[c["ys"]]), dweights, _sum_back(s["dxs"], s["row_of"], None).to(_DT[c["ys"]])
+
+
+# ----------------------------------------------------------------------------
+# the definition in 64 bits
+# ----------------------------------------------------------------------------
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    c, op = s["c"], s["op"]
+
+    def product(x, e):
+        """x [n, d_in] times one matrix's transpose, in 64 bits, a slice of output rows at a time."""
+        pick = (lambda t: t) if e is None else (lambda t: t[e])
+        codes, scales, zeros = pick(s["codes"]), pick(s["scales"]), None if s["zeros"] is None else pick(s["zeros"])
+        value = torch.arange(16, dtype=torch.float64, device=x.device)
+        if zeros is None:
+            value = torch.cat([value[:8], value[:8] - 8])
+        out = torch.empty(x.shape[0], codes.shape[0], dtype=torch.float64, device=x.device)
+        group = s["c"]["group"]
+        for a in range(0, codes.shape[0], 4096):
+            b = min(a + 4096, codes.shape[0])
+            w = torch.empty(b - a, codes.shape[1] * 2, dtype=torch.float64, device=x.device)
+            w[:, 0::2] = value[(codes[a:b] % 16).long()]
+            w[:, 1::2] = value[(codes[a:b] // 16).long()]
+            w = w.view(b - a, -1, group)
+            if zeros is not None:
+                w -= zeros[a:b, :, None].double()
+            w *= scales[a:b, :, None].double()
+            out[:, a:b] = x.double() @ w.view(b - a, -1).T
+        return out
+
+    if op == "base":
+        return product(s["x"], None)
+    if op == "experts":
+        y = torch.empty(s["y"].shape, dtype=torch.float64, device="cuda")
+        off = s["offsets"].tolist()
+        for e in range(c["E"]):
+            if off[e + 1] > off[e]:
+                slots = s["slot_of"][off[e]:off[e + 1]].long()
+                y[off[e]:off[e + 1]] = product(s["x"][torch.div(slots, c["k"], rounding_mode="floor")], e)
+        return y
+    if op == "step":
+        out = torch.zeros(c["T"], c["d_out"], dtype=torch.float64, device="cuda")
+        for e in range(c["E"]):
+            t, j = torch.nonzero(s["ids"] == e, as_tuple=True)
+            if t.numel():
+                out.index_add_(0, t, s["weights"][t, j].double()[:, None] * product(s["x"][t], e))
+        return out
+    if op == "dispatch":
+        flat = s["ids"].reshape(-1).long()
+        slots = torch.nonzero(flat >= 0)[:, 0]
+        slots = torch.sort(flat[slots] * flat.numel() + slots).values % flat.numel()  # by expert, then by slot
+        xs = torch.zeros(s["xs"].shape, dtype=torch.float64, device="cuda")
+        xs[:slots.numel()] = s["x"][torch.div(slots, c["k"], rounding_mode="floor")].double()
+        return None, None, None, xs  # the others are whole numbers
+    if op == "combine":
+        y = s["residual"].double()
+        for j in range(c["k"]):
+            t = torch.nonzero(s["row_of"][:, j] >= 0)[:, 0]
+            y[t] += s["weights"][t, j].double()[:, None] * s["ys"][s["row_of"][t, j].long()].double()
+        return y
+    dys = torch.zeros(c["T"] * c["k"], c["d"], dtype=torch.float64, device="cuda")
+    dweights = torch.zeros(c["T"], c["k"], dtype=torch.float64, device="cuda")
+    dx = torch.zeros(c["T"], c["d"], dtype=torch.float64, device="cuda")
+    for j in range(c["k"]):
+        t = torch.nonzero(s["row_of"][:, j] >= 0)[:, 0]
+        r = s["row_of"][t, j].long()
+        dys[r] = s["weights"][t, j].double()[:, None] * s["dy"][t].double()
+        dweights[t, j] = (s["ys"][r].double() * s["dy"][t].double()).sum(1)
+        dx[t] += s["dxs"][r].double()
+    return dys, dweights, dx
+
+
+# ----------------------------------------------------------------------------
+# what a pass cannot do without
+# ----------------------------------------------------------------------------
+
+def work(case):
+    c, op = case, case["op"]
+    T, ysz = c["T"], 2 if c["y"] == BF16 else 4
+    if op in ("base", "experts", "step"):
+        d_in, d_out, k = c["d_in"], c["d_out"], c.get("k", 1)
+        matrix = d_out * (d_in // 2 + d_in // c["group"] * ((2 if c["scales"] == BF16 else 4) + (1 if c["zeros"] else 0)))
+        hit = 1.0 if op == "base" else c["E"] * (1.0 - (1.0 - k / c["E"]) ** T)  # experts that get a row, on average
+        rows = T if op == "step" else T * k  # a step's expert rows need not reach memory
+        extra = 0 if op == "base" else 4 * T * k * (2 if op == "step" else 1)
+        return dict(bytes=hit * matrix + T * d_in * 2 + rows * d_out * ysz + extra, flops=2.0 * T * k * d_in * d_out)
+    k, d, kept = c["k"], c["d"], 1.0 - c["drop"]
+    rsz, slots = 2 if c["ys"] == BF16 else 4, T * k
+    if op == "dispatch":
+        return dict(bytes=12 * slots + 4 * (c["E"] + 1) + T * d * rsz + kept * slots * d * rsz, flops=0)
+    if op == "combine":
+        return dict(bytes=8 * slots + kept * slots * d * rsz + 2 * T * d * ysz, flops=2.0 * kept * slots * d)
+    return dict(bytes=12 * slots + kept * slots * d * rsz * 3 + T * d * (ysz + rsz), flops=4.0 * kept * slots * d)
