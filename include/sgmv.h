@@ -591,11 +591,127 @@ SGMV_API sgmv_status sgmv_lora_delta_noalloc(const void* x, int64_t ldx, int32_t
                                              void* y, int64_t ldy, int32_t y_dtype,
                                              sgmv_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Base products from 4-bit weights                                          */
+/* ------------------------------------------------------------------------ */
+/*
+ * The base output W x that the delta is added to ([SGMV post], "The bare
+ * mechanism", y = Wx + B(Ax)), from a base kept in 4 bits ([SGMV post],
+ * "Combined pattern with quantisation and disaggregated serving": the base
+ * quantised, the adapters in BF16):
+ *
+ *   y[t][n] <- round( sum_g s[n][g] * sum_{c in group g} (q[n][c] - z[n][g]) * x[t][c] )
+ *
+ * codes    device [d_out][d_in / 2] bytes, 16-byte aligned: value 2i in the low
+ *          nibble of byte i (the pool's INT4 order).  Without zeros a code is
+ *          two's complement, -8..7; with zeros it is unsigned, 0..15.
+ * scales   device [d_out][d_in / group], scale_dtype 0 = bf16, 1 = fp32
+ * zeros    device uint8 [d_out][d_in / group], each 0..15, or NULL
+ * group    32, 64 or 128 values; d_in is a multiple of it
+ * x        device bf16 [T][ldx], ldx >= d_in, row starts 16-byte aligned
+ * y        device [T][ldy], ldy >= d_out, y_dtype 0 = bf16, 1 = fp32; aligned to
+ *          its type.  It is written, not accumulated into, and may not overlap x.
+ * T >= 0 and d_out >= 1 are any.  The products are exact in fp32 (codes and x
+ * are bf16 values), summed in fp32, the scale applied in fp32 per group and the
+ * result rounded once; the order of the sum is fixed for given sizes, so a call
+ * repeats bit for bit.  The pointers belong to the current device.
+ */
+SGMV_API sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, int32_t d_in, int32_t d_out,
+                                       const void* codes, const void* scales, int32_t scale_dtype,
+                                       const uint8_t* zeros, int32_t group, void* y, int64_t ldy,
+                                       int32_t y_dtype, sgmv_stream_t stream);
+/*
+ * The same with one matrix per expert: codes, scales and zeros have a leading
+ * dimension n_experts (1..4096), and row i of y, offsets[e] <= i < offsets[e+1],
+ * is W_e times row i of x -- or, with slot_of, times row slot_of[i] / k of x, so
+ * that the tokens need not be gathered first.
+ * offsets  device int32 [n_experts + 1], ascending from 0, last <= rows
+ * slot_of  device int32 [rows] (sgmv_expert_order), or NULL; k: choices per token
+ * rows     rows of y; x_rows: rows of x (>= rows without slot_of)
+ * Rows of y from offsets[n_experts] on are left as they were.  A slot whose
+ * token is not a row of x is reported by sgmv_check_errors and its row left
+ * unwritten; offsets that do not ascend from 0 to at most rows are reported, and
+ * no row outside y is touched.
+ */
+SGMV_API sgmv_status sgmv_base_product_experts(const void* x, int64_t ldx, int32_t x_rows, int32_t d_in,
+                                               int32_t d_out, int32_t n_experts, const void* codes,
+                                               const void* scales, int32_t scale_dtype, const uint8_t* zeros,
+                                               int32_t group, const int32_t* offsets, const int32_t* slot_of,
+                                               int32_t k, int32_t rows, void* y, int64_t ldy, int32_t y_dtype,
+                                               sgmv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Tokens sorted by expert and back                                          */
+/* ------------------------------------------------------------------------ */
+/*
+ * For batches whose tokens use several experts each (or several adapters: a
+ * plan over the sorted rows has one segment per expert).  Slot t * k + j is
+ * choice j of token t.
+ *
+ * The stable sort of the slots by expert: row_of[t][j] is the slot's row in that
+ * order (ascending expert, then ascending slot), slot_of its inverse, and
+ * expert e has rows offsets[e] .. offsets[e+1].
+ * expert_ids device int32 [T][k]: 0..n_experts-1, or -1 for a slot without an
+ *            expert, which gets row_of = -1 and no row.  Any other id is treated
+ *            as -1 and reported by sgmv_check_errors.  A token may name an expert
+ *            twice.
+ * offsets    device int32 [n_experts + 1]
+ * row_of     device int32 [T][k]
+ * slot_of    device int32 [T * k]; -1 from offsets[n_experts] on
+ * workspace  device, 4-byte aligned, of the bytes sgmv_expert_order_workspace
+ *            gives (0: may be NULL; -1: refused sizes); nothing in it is kept
+ *            from call to call, but two calls that may overlap need two.
+ * k is 1..64, n_experts 1..4096, T * k at most 2^30.
+ */
+SGMV_API int64_t sgmv_expert_order_workspace(int32_t T, int32_t k, int32_t n_experts);
+SGMV_API sgmv_status sgmv_expert_order(const int32_t* expert_ids, int32_t T, int32_t k, int32_t n_experts,
+                                       int32_t* offsets, int32_t* row_of, int32_t* slot_of, void* workspace,
+                                       int64_t workspace_bytes, sgmv_stream_t stream);
+/*
+ * xs[row_of[t][j]] <- x[t] for every slot with a row; other rows of xs are left
+ * as they were.  x and xs are device [T][ldx] and [rows][ldxs] of d values,
+ * dtype 0 = bf16, 1 = fp32, aligned to their type (rows that all start on 16
+ * bytes are copied faster).  row_of comes from sgmv_expert_order: no row twice.
+ * A row outside 0..rows-1 other than -1 is skipped and reported.
+ */
+SGMV_API sgmv_status sgmv_expert_gather(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t dtype,
+                                        const int32_t* row_of, int32_t k, void* xs, int64_t ldxs, int32_t rows,
+                                        sgmv_stream_t stream);
+/* Its gradient: dx[t] <- round( sum_j dxs[row_of[t][j]] ), summed in fp32 over the
+ * slots with a row in the order of j (0 for a token without any). */
+SGMV_API sgmv_status sgmv_expert_gather_backward(const void* dxs, int64_t lddxs, int32_t rows, int32_t T, int32_t d,
+                                                 int32_t dtype, const int32_t* row_of, int32_t k, void* dx,
+                                                 int64_t lddx, sgmv_stream_t stream);
+/*
+ * y[t] <- round( add[t] + sum_j weights[t][j] * ys[row_of[t][j]] ) over the slots
+ * with a row, in fp32 in the order of j.  Values of slots without a row, and
+ * their weights, are not read.
+ * ys      device [rows][ldys], ys_dtype; y and add device [T][ldy], [T][ldadd],
+ *         y_dtype; dtypes 0 = bf16, 1 = fp32.  add may be NULL (0) or y itself.
+ * weights device fp32 [T][k], or NULL (1)
+ */
+SGMV_API sgmv_status sgmv_expert_combine(const void* ys, int64_t ldys, int32_t rows, int32_t ys_dtype,
+                                         const int32_t* row_of, const float* weights, int32_t T, int32_t k,
+                                         int32_t d, const void* add, int64_t ldadd, void* y, int64_t ldy,
+                                         int32_t y_dtype, sgmv_stream_t stream);
+/*
+ * Its gradients (add's is dy itself), dys of ys's dtype, each NULL when not wanted:
+ *   dys[row_of[t][j]] <- round( weights[t][j] * dy[t] )   (other rows are left as they were)
+ *   dweights[t][j]    <- sum_c dy[t][c] * ys[row_of[t][j]][c]   (fp32; 0 for a slot without a row)
+ * ys is read only for dweights.  dys may not overlap ys or dy.
+ */
+SGMV_API sgmv_status sgmv_expert_combine_backward(const void* dy, int64_t lddy, int32_t dy_dtype, const void* ys,
+                                                  int64_t ldys, int32_t rows, int32_t ys_dtype,
+                                                  const int32_t* row_of, const float* weights, int32_t T,
+                                                  int32_t k, int32_t d, void* dys, int64_t lddys, float* dweights,
+                                                  sgmv_stream_t stream);
+
 /*
  * Wait for `stream`, then return and clear the device error word:
  * SGMV_OK, SGMV_ERR_BOUNDS or SGMV_ERR_TIMEOUT.  *flags (may be NULL) receives
  * the raw bits (1 = page id out of range, 2 = token row out of range,
- * 4 = wait timed out, 8 = segment rows out of range).
+ * 4 = wait timed out, 8 = segment or expert rows out of range, 16 = expert id
+ * or expert offset out of range).
  */
 SGMV_API sgmv_status sgmv_check_errors(sgmv_stream_t stream, uint32_t* flags);
 

@@ -39,7 +39,9 @@ EXPORTED = ("sgmv_status_string", "sgmv_last_error", "sgmv_pool_create", "sgmv_p
             "sgmv_lora_delta_host",
             "sgmv_check_errors", "sgmv_residency_create", "sgmv_residency_destroy",
             "sgmv_residency_register", "sgmv_residency_unregister", "sgmv_residency_prepare",
-            "sgmv_residency_get_stats")
+            "sgmv_residency_get_stats", "sgmv_base_product", "sgmv_base_product_experts",
+            "sgmv_expert_order_workspace", "sgmv_expert_order", "sgmv_expert_gather", "sgmv_expert_gather_backward",
+            "sgmv_expert_combine", "sgmv_expert_combine_backward")
 
 
 class SgmvError(RuntimeError):
@@ -136,6 +138,16 @@ def load_library() -> ctypes.CDLL:
         "sgmv_residency_unregister": (st, [vp, i32]),
         "sgmv_residency_prepare": (st, [vp, vp, i32, vp, vp, ctypes.POINTER(i32)]),
         "sgmv_residency_get_stats": (st, [vp, ctypes.POINTER(ResidencyStats)]),
+        "sgmv_base_product": (st, [vp, i64, i32, i32, i32, vp, vp, i32, vp, i32, vp, i64, i32, vp]),
+        "sgmv_base_product_experts": (st, [vp, i64, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, i32, i32, vp,
+                                           i64, i32, vp]),
+        "sgmv_expert_order_workspace": (i64, [i32, i32, i32]),
+        "sgmv_expert_order": (st, [vp, i32, i32, i32, vp, vp, vp, vp, i64, vp]),
+        "sgmv_expert_gather": (st, [vp, i64, i32, i32, i32, vp, i32, vp, i64, i32, vp]),
+        "sgmv_expert_gather_backward": (st, [vp, i64, i32, i32, i32, i32, vp, i32, vp, i64, vp]),
+        "sgmv_expert_combine": (st, [vp, i64, i32, i32, vp, vp, i32, i32, i32, vp, i64, vp, i64, i32, vp]),
+        "sgmv_expert_combine_backward": (st, [vp, i64, i32, vp, i64, i32, i32, vp, vp, i32, i32, i32, vp, i64, vp,
+                                              vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -663,3 +675,222 @@ def lora_delta(x: torch.Tensor, plan: BatchPlan, pool: AdapterPool, y: torch.Ten
         plan.table_ptr(stream), pool.handle, float(scale), _ptr(y), y.stride(0),
         0 if y.dtype == torch.bfloat16 else 1, _ptr(v), v.stride(0), _stream(stream)))
     return v
+
+
+# ---------------------------------------------------------------------------
+# base products from 4-bit weights, and tokens sorted by expert
+# ---------------------------------------------------------------------------
+
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _mat(t: torch.Tensor, name: str, device) -> Tuple[int, int]:
+    """(address, row stride) of a bf16 or fp32 matrix on `device` whose rows are contiguous."""
+    _need(t.dtype in _DTYPE and t.dim() == 2 and t.device == device, f"{name} must be a bf16 or fp32 matrix on {device}")
+    rows, cols = t.shape
+    _need(cols <= 1 or rows == 0 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else (cols + 7) // 8 * 8)
+
+
+def _flat(t: torch.Tensor, name: str, dtype, device) -> int:
+    """Address of a contiguous tensor of `dtype` on `device`."""
+    _need(t.dtype == dtype and t.device == device and t.is_contiguous(), f"{name} must be a contiguous {dtype} tensor on {device}")
+    return t.data_ptr()
+
+
+def _here(t: torch.Tensor, name: str):
+    """The device of `t`, which has to be the current CUDA device."""
+    d = t.device
+    _need(d.type == "cuda" and d.index == torch.cuda.current_device(), f"{name} must be on the current CUDA device")
+    return d
+
+
+def _weights4(codes, scales, zeros, lead: int, device):
+    """Checks and addresses of a 4-bit matrix: codes [.., d_out, d_in / 2], scales and zeros [.., d_out, d_in / group]."""
+    pc = _flat(codes, "codes", torch.uint8, device)
+    _need(codes.dim() == 2 + lead and scales.dim() == 2 + lead and scales.shape[:-1] == codes.shape[:-1],
+          "codes and scales must have the same leading dimensions")
+    _need(scales.dtype in _DTYPE, "scales must be bf16 or fp32")
+    ps = _flat(scales, "scales", scales.dtype, device)
+    d_in, n_groups = 2 * codes.shape[-1], scales.shape[-1]
+    _need(n_groups > 0 and d_in % n_groups == 0, "d_in must be a multiple of the number of groups")
+    pz = None
+    if zeros is not None:
+        pz = _flat(zeros, "zeros", torch.uint8, device)
+        _need(zeros.shape == scales.shape, "zeros must have the shape of scales")
+    return pc, ps, _DTYPE[scales.dtype], pz, d_in, d_in // n_groups
+
+
+def base_product(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor, zeros=None,
+                 stream=None) -> torch.Tensor:
+    """y[t, n] = sum_g scales[n, g] sum_{c in g} (code(n, c) - zeros[n, g]) x[t, c]: the base output from
+    4-bit weights.  codes: uint8 [d_out, d_in / 2], value 2i in the low nibble of byte i, two's
+    complement without zeros and unsigned with them; scales: bf16 or fp32 [d_out, d_in / group], group
+    32, 64 or 128; zeros: uint8 like scales; x: bf16 [T, d_in]; y: bf16 or fp32 [T, d_out].  Returns y."""
+    dev = _here(x, "x")
+    pc, ps, sdt, pz, d_in, group = _weights4(codes, scales, zeros, 0, dev)
+    px, ldx = _mat(x, "x", dev)
+    py, ldy = _mat(y, "y", dev)
+    T, d_out = x.shape[0], codes.shape[0]
+    _need(x.dtype == torch.bfloat16 and x.shape[1] == d_in, "x must be bf16 [T, d_in]")
+    _need(y.shape[0] == T and y.shape[1] == d_out, "y must be [T, d_out]")
+    _check(load_library().sgmv_base_product(px, ldx, T, d_in, d_out, pc, ps, sdt, pz, group, py, ldy, _DTYPE[y.dtype],
+                                            _stream(stream)))
+    return y
+
+
+def base_product_experts(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
+                         y: torch.Tensor, zeros=None, slot_of: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """base_product with one matrix per expert (a leading dimension of codes, scales and zeros): row i
+    of y, offsets[e] <= i < offsets[e + 1], is W_e times row i of x, or with slot_of (expert_order)
+    times the slot's token.  Rows from offsets[-1] on are left as they were.  Returns y."""
+    dev = _here(x, "x")
+    pc, ps, sdt, pz, d_in, group = _weights4(codes, scales, zeros, 1, dev)
+    px, ldx = _mat(x, "x", dev)
+    py, ldy = _mat(y, "y", dev)
+    n_experts, d_out, _ = codes.shape
+    x_rows, rows = x.shape[0], y.shape[0]
+    _need(x.dtype == torch.bfloat16 and x.shape[1] == d_in, "x must be bf16 [.., d_in]")
+    _need(y.shape[1] == d_out, "y must be [rows, d_out]")
+    po = _flat(offsets, "offsets", torch.int32, dev)
+    _need(offsets.numel() == n_experts + 1, "offsets must have one value per expert and one more")
+    psl, k = None, 1
+    if slot_of is not None:
+        psl = _flat(slot_of, "slot_of", torch.int32, dev)
+        _need(slot_of.numel() == rows and (rows % x_rows == 0 if x_rows else rows == 0),
+              "slot_of must have a slot for every row of y, k for every row of x")
+        k = rows // x_rows if rows else 1
+    else:
+        _need(x_rows == rows, "x and y must have the same rows without slot_of")
+    _check(load_library().sgmv_base_product_experts(px, ldx, x_rows, d_in, d_out, n_experts, pc, ps, sdt, pz, group, po,
+                                                    psl, k, rows, py, ldy, _DTYPE[y.dtype], _stream(stream)))
+    return y
+
+
+def expert_order(expert_ids: torch.Tensor, n_experts: int, offsets: Optional[torch.Tensor] = None,
+                 row_of: Optional[torch.Tensor] = None, slot_of: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None):
+    """The stable sort of a batch's slots by expert.  expert_ids: int32 [T, k], -1 = no expert.  Returns
+    (offsets [n_experts + 1], row_of [T, k], slot_of [T * k]), int32, into the tensors given or new ones;
+    `workspace`: at least expert_order_workspace(T, k, n_experts) bytes, or taken from torch's allocator."""
+    dev = _here(expert_ids, "expert_ids")
+    pi = _flat(expert_ids, "expert_ids", torch.int32, dev)
+    _need(expert_ids.dim() == 2, "expert_ids must be [T, k]")
+    T, k = expert_ids.shape
+    lib = load_library()
+    made = []
+    if offsets is None:
+        offsets = torch.empty(max(int(n_experts), 0) + 1, dtype=torch.int32, device=dev)
+        made.append(offsets)
+    if row_of is None:
+        row_of = torch.empty_like(expert_ids)
+        made.append(row_of)
+    if slot_of is None:
+        slot_of = torch.empty(T * k, dtype=torch.int32, device=dev)
+        made.append(slot_of)
+    _need(offsets.numel() == n_experts + 1 and row_of.shape == expert_ids.shape and slot_of.numel() == T * k,
+          "offsets, row_of and slot_of must have n_experts + 1, [T, k] and T * k values")
+    need = lib.sgmv_expert_order_workspace(T, k, n_experts)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    if stream is not None and made:      # their memory may be reused by the current stream only after `stream`
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        for t in made:
+            t.record_stream(s)
+    pw, nw = (None, 0) if workspace is None else (_flat(workspace, "workspace", workspace.dtype, dev),
+                                                  workspace.numel() * workspace.element_size())
+    _check(lib.sgmv_expert_order(pi, T, k, n_experts, _flat(offsets, "offsets", torch.int32, dev),
+                                 _flat(row_of, "row_of", torch.int32, dev), _flat(slot_of, "slot_of", torch.int32, dev),
+                                 pw, nw, _stream(stream)))
+    return offsets, row_of, slot_of
+
+
+def expert_order_workspace(T: int, k: int, n_experts: int) -> int:
+    """Bytes of workspace that expert_order takes for these sizes (-1: refused sizes)."""
+    return int(load_library().sgmv_expert_order_workspace(int(T), int(k), int(n_experts)))
+
+
+def _rows_of(row_of: torch.Tensor, device) -> Tuple[int, int, int]:
+    _need(row_of.dim() == 2, "row_of must be [T, k]")
+    return _flat(row_of, "row_of", torch.int32, device), row_of.shape[0], row_of.shape[1]
+
+
+def expert_gather(x: torch.Tensor, row_of: torch.Tensor, xs: torch.Tensor, stream=None) -> torch.Tensor:
+    """xs[row_of[t, j]] = x[t] for every slot with a row (row_of from expert_order); other rows of xs are
+    left as they were.  x, xs: bf16 or fp32, one dtype.  Returns xs."""
+    dev = _here(x, "x")
+    pr, T, k = _rows_of(row_of, dev)
+    px, ldx = _mat(x, "x", dev)
+    ps, lds = _mat(xs, "xs", dev)
+    _need(x.dtype == xs.dtype and x.shape[0] == T and x.shape[1] == xs.shape[1], "x [T, d] and xs [rows, d] must have one dtype and d")
+    _check(load_library().sgmv_expert_gather(px, ldx, T, x.shape[1], _DTYPE[x.dtype], pr, k, ps, lds, xs.shape[0],
+                                             _stream(stream)))
+    return xs
+
+
+def expert_gather_backward(dxs: torch.Tensor, row_of: torch.Tensor, dx: torch.Tensor, stream=None) -> torch.Tensor:
+    """dx[t] = sum_j dxs[row_of[t, j]], the gradient of expert_gather.  Returns dx."""
+    dev = _here(dx, "dx")
+    pr, T, k = _rows_of(row_of, dev)
+    ps, lds = _mat(dxs, "dxs", dev)
+    px, ldx = _mat(dx, "dx", dev)
+    _need(dx.dtype == dxs.dtype and dx.shape[0] == T and dx.shape[1] == dxs.shape[1], "dx [T, d] and dxs [rows, d] must have one dtype and d")
+    _check(load_library().sgmv_expert_gather_backward(ps, lds, dxs.shape[0], T, dx.shape[1], _DTYPE[dx.dtype], pr, k, px,
+                                                      ldx, _stream(stream)))
+    return dx
+
+
+def expert_combine(ys: torch.Tensor, row_of: torch.Tensor, y: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                   add: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[t] = add[t] + sum_j weights[t, j] ys[row_of[t, j]] over the slots with a row, in fp32, rounded
+    once.  weights: fp32 [T, k] or None (1); add: like y, None (0) or y itself.  Returns y."""
+    dev = _here(y, "y")
+    pr, T, k = _rows_of(row_of, dev)
+    ps, lds = _mat(ys, "ys", dev)
+    py, ldy = _mat(y, "y", dev)
+    _need(y.shape[0] == T and y.shape[1] == ys.shape[1], "y must be [T, d] and ys [rows, d]")
+    pw = pa = None
+    lda = 0
+    if weights is not None:
+        pw = _flat(weights, "weights", torch.float32, dev)
+        _need(weights.shape == row_of.shape, "weights must have the shape of row_of")
+    if add is not None:
+        pa, lda = _mat(add, "add", dev)
+        _need(add.shape == y.shape and add.dtype == y.dtype, "add must have the shape and dtype of y")
+    _check(load_library().sgmv_expert_combine(ps, lds, ys.shape[0], _DTYPE[ys.dtype], pr, pw, T, k, y.shape[1], pa, lda,
+                                              py, ldy, _DTYPE[y.dtype], _stream(stream)))
+    return y
+
+
+def expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, row_of: torch.Tensor,
+                            weights: Optional[torch.Tensor], dys: Optional[torch.Tensor] = None,
+                            dweights: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of expert_combine: dys[row_of[t, j]] = weights[t, j] dy[t] (other rows are left as
+    they were) and dweights[t, j] = <dy[t], ys[row_of[t, j]]> (0 for a slot without a row); each is
+    computed into the tensor given and left out where None.  Returns (dys, dweights)."""
+    dev = _here(dy, "dy")
+    pr, T, k = _rows_of(row_of, dev)
+    pd, ldd = _mat(dy, "dy", dev)
+    ps, lds = _mat(ys, "ys", dev)
+    _need(dy.shape[0] == T and dy.shape[1] == ys.shape[1], "dy must be [T, d] and ys [rows, d]")
+    pw = pg = pdw = None
+    ldg = 0
+    if weights is not None:
+        pw = _flat(weights, "weights", torch.float32, dev)
+        _need(weights.shape == row_of.shape, "weights must have the shape of row_of")
+    if dys is not None:
+        pg, ldg = _mat(dys, "dys", dev)
+        _need(dys.shape == ys.shape and dys.dtype == ys.dtype, "dys must have the shape and dtype of ys")
+    if dweights is not None:
+        pdw = _flat(dweights, "dweights", torch.float32, dev)
+        _need(dweights.shape == row_of.shape, "dweights must have the shape of row_of")
+    _check(load_library().sgmv_expert_combine_backward(pd, ldd, _DTYPE[dy.dtype], ps, lds, ys.shape[0], _DTYPE[ys.dtype],
+                                                       pr, pw, T, k, dy.shape[1], pg, ldg, pdw, _stream(stream)))
+    return dys, dweights

@@ -1,0 +1,36 @@
+// Declarations shared by the expert operators and the 4-bit base products.
+#pragma once
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace sgmv {
+
+constexpr int kMaxExperts = 4096;      // experts of one order / one base product
+constexpr int kMaxExpertsPerToken = 64;
+constexpr int64_t kMaxSlots = 1 << 30; // token-expert slots of one order
+
+// Device error bit of these operators, beside those of ptx.cuh.
+enum : uint32_t { kErrExpert = 16u };  // expert id or expert offset out of range
+
+// Read and clear the device error words of the two translation units.
+cudaError_t read_clear_errors_experts(uint32_t* bits, cudaStream_t stream);
+cudaError_t read_clear_errors_base(uint32_t* bits, cudaStream_t stream);
+
+// y = W x for rows of 4-bit codes; see sgmv_base_product in include/sgmv.h.
+struct BaseArgs {
+    const uint16_t* x;        // bf16 [rows of x][ldx]
+    int64_t ldx;
+    const uint8_t* codes;     // [experts][d_out][d_in / 2]
+    const void* scales;       // [experts][d_out][d_in / group], bf16 or fp32
+    const uint8_t* zeros;     // the same shape, or null
+    void* y;                  // [rows][ldy], bf16 or fp32
+    int64_t ldy;
+    const int32_t* offsets;   // [experts + 1] rows of each expert, or null: one matrix, all rows
+    const int32_t* slot_of;   // [rows] slot of each row (x row = slot / k), or null: x row = row
+    int32_t rows, x_rows, k, experts, d_in, d_out, group;
+};
+
+}  // namespace sgmv

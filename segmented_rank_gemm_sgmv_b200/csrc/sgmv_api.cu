@@ -5,6 +5,7 @@
 #include <mutex>
 #include <string>
 
+#include "experts.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -658,6 +659,8 @@ extern "C" sgmv_status sgmv_check_errors(sgmv_stream_t stream_, uint32_t* flags)
     uint32_t bits = 0;
     SGMV_CUDA_TRY(read_clear_errors_simt(&bits, stream));
     SGMV_CUDA_TRY(read_clear_errors_tc(&bits, stream));
+    SGMV_CUDA_TRY(read_clear_errors_experts(&bits, stream));
+    SGMV_CUDA_TRY(read_clear_errors_base(&bits, stream));
     if (flags) *flags = bits;
     if (bits & kErrTimeout) return fail(SGMV_ERR_TIMEOUT, "a device-side wait timed out");
     if (bits) return fail(SGMV_ERR_BOUNDS, "a device-side bounds check failed");

@@ -1,0 +1,480 @@
+// Tokens sorted by expert and back: the order of a batch's (token, choice) slots by expert, the
+// gather of the tokens into that order, the weighted sum of the experts' rows back into token
+// order, and the gradients of the last two.
+#include <algorithm>
+#include <string>
+
+#include "experts.h"
+#include "ptx.cuh"
+
+namespace sgmv {
+
+__device__ unsigned int g_err_experts;
+
+namespace {
+
+constexpr int kOrderThreads = 512, kOrderWarps = kOrderThreads / 32;
+constexpr int kOrderTile = 2048;       // slots of a block when there are several
+constexpr int kOrderMaxBlocks = 148;   // one wave of blocks
+constexpr int kOrderCounts = 65536;    // most block counts that the second kernel's blocks each read
+
+// Blocks that a sort of n slots takes: one while that is quick, else tiles of at least kOrderTile
+// slots in at most one wave, and no more counts (blocks x experts) than kOrderCounts.
+int order_blocks(int64_t n, int experts) {
+    if (n <= 2 * kOrderTile) return 1;
+    const int64_t most = std::min<int64_t>(kOrderMaxBlocks, std::max(1, kOrderCounts / experts));
+    return (int)std::min<int64_t>(most, (n + kOrderTile - 1) / kOrderTile);
+}
+
+// Warps of the ordering kernel: each keeps a count per expert in shared memory.
+int order_warps(int experts) { return experts <= 2048 ? kOrderWarps : kOrderWarps / 2; }
+
+__device__ __forceinline__ int load_id(const int32_t* ids, int64_t i, int64_t end, int experts) {
+    if (i >= end) return -1;
+    const int id = ids[i];
+    if (id >= 0 && id < experts) return id;
+    if (id != -1) atomicOr(&g_err_experts, kErrExpert);
+    return -1;
+}
+
+// Slots of each expert in each block's tile.
+__global__ void __launch_bounds__(kOrderThreads) order_count_kernel(const int32_t* ids, int64_t n, int64_t tile,
+                                                                    int experts, int32_t* counts) {
+    extern __shared__ int32_t hist[];
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+    const int64_t begin = blockIdx.x * tile, end = min(n, begin + tile);
+    for (int64_t i = begin + threadIdx.x; i < end; i += blockDim.x) {
+        const int id = load_id(ids, i, end, experts);
+        if (id >= 0) atomicAdd(&hist[id], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) counts[(int64_t)blockIdx.x * experts + e] = hist[e];
+}
+
+// A stable counting sort: a slot's row is the number of slots of lower experts, plus those of its own
+// expert in earlier blocks (from the counts), in earlier warps of this block, and earlier in its own
+// warp.  Each warp owns a contiguous run of the block's slots and its own counts, so nothing depends on
+// the order in which warps run.
+__global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* ids, int64_t n, int64_t tile, int experts,
+                                                              const int32_t* counts, int32_t* offsets, int32_t* row_of,
+                                                              int32_t* slot_of) {
+    extern __shared__ int32_t smem[];
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    int32_t* hist = smem;                      // [warps][experts]
+    int32_t* total = smem + warps * experts;   // [experts] slots of all blocks, then the first row
+    int32_t* sums = total + experts;           // [warps + 1]
+    for (int i = threadIdx.x; i < warps * experts; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    const int64_t begin = blockIdx.x * tile, end = min(n, begin + tile);
+    const int64_t per = ((tile + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t w0 = begin + warp * per, w1 = min(end, w0 + per);
+    int32_t* mine = hist + warp * experts;
+    for (int64_t i = w0; i < w1; i += 32) {
+        const int id = load_id(ids, i + lane, w1, experts);
+        const unsigned same = __match_any_sync(0xffffffffu, id);
+        if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // per expert: the counts of this block's warps become the rows before each warp's
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) {
+        int32_t here = 0;
+        for (int w = 0; w < warps; ++w) {
+            const int32_t c = hist[w * experts + e];
+            hist[w * experts + e] = here;
+            here += c;
+        }
+        int32_t before = 0, all = here;
+        if (gridDim.x > 1) {
+            all = 0;
+#pragma unroll 8
+            for (int b = 0; b < (int)gridDim.x; ++b) {
+                const int32_t c = counts[(int64_t)b * experts + e];
+                all += c;
+                before += b < (int)blockIdx.x ? c : 0;
+            }
+        }
+        total[e] = all;
+        for (int w = 0; w < warps; ++w) hist[w * experts + e] += before;
+    }
+    __syncthreads();
+    // exclusive scan of the totals over the experts: each thread scans a run of them
+    const int run = (experts + blockDim.x - 1) / blockDim.x;
+    const int e0 = min(experts, (int)threadIdx.x * run), e1 = min(experts, e0 + run);
+    int32_t s = 0;
+    for (int e = e0; e < e1; ++e) s += total[e];
+    int32_t incl = s;
+    for (int o = 1; o < 32; o *= 2) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int32_t first = incl - s;
+    for (int w = 0; w < warp; ++w) first += sums[w];
+    for (int e = e0; e < e1; ++e) {
+        const int32_t c = total[e];
+        total[e] = first;
+        if (blockIdx.x == 0) offsets[e] = first;
+        first += c;
+    }
+    if (threadIdx.x == blockDim.x - 1) {       // the last thread's run ends at the last expert
+        sums[warps] = first;
+        if (blockIdx.x == 0) offsets[experts] = first;
+    }
+    __syncthreads();
+    for (int64_t i = w0; i < w1; i += 32) {
+        const int id = load_id(ids, i + lane, w1, experts);
+        const unsigned same = __match_any_sync(0xffffffffu, id);
+        int32_t row = -1;
+        if (id >= 0) row = total[id] + mine[id] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
+        __syncwarp();
+        if (i + lane < w1) {
+            row_of[i + lane] = row;
+            if (row >= 0) slot_of[row] = (int32_t)(i + lane);
+        }
+    }
+    const int32_t kept = sums[warps];
+    for (int64_t r = begin + threadIdx.x; r < end; r += blockDim.x)
+        if (r >= kept) slot_of[r] = -1;
+}
+
+// ------------------------------------------------------------------ rows
+constexpr int kRowThreads = 256;
+
+// The row of slot i, or -1: a dropped slot, or a row outside the buffer (reported).
+__device__ __forceinline__ int load_row(const int32_t* row_of, int64_t i, int32_t rows) {
+    const int r = row_of[i];
+    if (r >= 0 && r < rows) return r;
+    if (r != -1) atomicOr(&g_err_experts, kErrRows);
+    return -1;
+}
+
+// xs[row_of[t][j]] = x[t]: a block copies one chunk of one token's row to its k places, so x is read once.
+// U is the unit of the copy: 16 bytes where both sides allow it, else one element.
+template <typename U>
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(const U* x, int64_t ldx, int32_t units, int32_t chunks,
+                                                             const int32_t* row_of, int32_t k, U* xs, int64_t ldxs,
+                                                             int32_t rows) {
+    const int64_t t = blockIdx.x / chunks;
+    const int u0 = (int)(blockIdx.x % chunks) * (2 * kRowThreads) + threadIdx.x, u1 = u0 + kRowThreads;
+    U a{}, b{};
+    if (u0 < units) a = x[t * ldx + u0];
+    if (u1 < units) b = x[t * ldx + u1];
+    for (int j = 0; j < k; ++j) {
+        const int64_t r = load_row(row_of, t * k + j, rows);
+        if (r < 0) continue;
+        if (u0 < units) xs[r * ldxs + u0] = a;
+        if (u1 < units) xs[r * ldxs + u1] = b;
+    }
+}
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<uint16_t>(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// V consecutive values, as 16-byte loads and stores where V > 1.
+template <typename T, int V>
+__device__ __forceinline__ void load_vals(const T* p, float (&f)[V]) {
+    if constexpr (V == 1) {
+        f[0] = to_f32<T>(*p);
+    } else if constexpr (sizeof(T) == 2) {
+        static_assert(V == 8, "eight values a unit");
+        unpack8(*reinterpret_cast<const uint4*>(p), f);
+    } else {
+        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vals(T* p, const float (&f)[V]) {
+    if constexpr (V == 1) {
+        *p = from_f32<T>(f[0]);
+    } else if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                  pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+
+// y[t] = add[t] + sum_j w[t][j] ys[row_of[t][j]], summed in fp32 in the order of j and rounded once.
+// Without weights every w is 1 (the gather's gradient).  V = 8 where every row starts on 16 bytes and d is
+// a multiple of 8, else 1.
+template <typename TI, typename TO, int V>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const TI* ys, int64_t ldys, int32_t rows,
+                                                              const int32_t* row_of, const float* w, int32_t k,
+                                                              int32_t d, int32_t chunks, const TO* add, int64_t ldadd,
+                                                              TO* y, int64_t ldy) {
+    const int64_t t = blockIdx.x / chunks;
+    const int c = ((int)(blockIdx.x % chunks) * kRowThreads + threadIdx.x) * V;
+    if (c >= d) return;
+    float acc[V], f[V];
+    if (add) {
+        load_vals<TO, V>(add + t * ldadd + c, acc);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    }
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) {
+        const int64_t r = load_row(row_of, t * k + j, rows);
+        if (r < 0) continue;
+        const float wj = w ? w[t * k + j] : 1.0f;
+        load_vals<TI, V>(ys + r * ldys + c, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
+    }
+    store_vals<TO, V>(y + t * ldy + c, acc);
+}
+
+// One slot (t, j) a block: dys[row] = w[t][j] dy[t], dw[t][j] = sum_c dy[t][c] ys[row][c].  Each thread sums
+// its columns in ascending order, then the block's sums are added in a fixed tree: the same bits every run.
+template <typename TI, typename TO, int V>
+__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const TO* dy, int64_t lddy, const TI* ys,
+                                                                       int64_t ldys, int32_t rows,
+                                                                       const int32_t* row_of, const float* w, int32_t k,
+                                                                       int32_t d, TI* dys, int64_t lddys, float* dw) {
+    const int64_t slot = blockIdx.x, t = slot / k;
+    const int64_t r = load_row(row_of, slot, rows);
+    if (r < 0) {
+        if (dw && threadIdx.x == 0) dw[slot] = 0.0f;
+        return;
+    }
+    const float wj = w ? w[slot] : 1.0f;
+    float sum = 0.0f, g[V], f[V];
+    for (int c = threadIdx.x * V; c < d; c += kRowThreads * V) {
+        load_vals<TO, V>(dy + t * lddy + c, g);
+        if (dw) {
+            load_vals<TI, V>(ys + r * ldys + c, f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum = fmaf(g[i], f[i], sum);
+        }
+        if (dys) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[i] *= wj;
+            store_vals<TI, V>(dys + r * lddys + c, g);
+        }
+    }
+    if (!dw) return;
+    __shared__ float part[kRowThreads / 32];
+    for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kRowThreads / 32; ++i) sum += part[i];
+        dw[slot] = sum;
+    }
+}
+
+bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
+// Every row of a matrix starts on 16 bytes (a null matrix does).
+bool rows16(const void* p, int64_t ld, int64_t esz) { return aligned(p, 16) && (ld * esz) % 16 == 0; }
+
+// What the row operators have in common.
+sgmv_status check_rows(const char* who, int32_t T, int32_t k, int32_t d, int32_t rows, const int32_t* row_of) {
+    const std::string w(who);
+    if (T < 0 || d < 1 || rows < 0) return fail(SGMV_ERR_INVALID, w + ": T, rows >= 0 and d >= 1 are required");
+    if (k < 1 || k > kMaxExpertsPerToken) return fail(SGMV_ERR_INVALID, w + ": k must be in 1..64");
+    if ((int64_t)T * k > kMaxSlots) return fail(SGMV_ERR_UNSUPPORTED, w + ": T * k must be at most 2^30");
+    if (T > 0 && (!row_of || !aligned(row_of, 4)))
+        return fail(SGMV_ERR_INVALID, w + ": row_of is required, 4-byte aligned");
+    return SGMV_OK;
+}
+sgmv_status check_matrix(const char* who, const char* name, const void* p, int64_t ld, int32_t d, int64_t esz) {
+    if (!p || !aligned(p, esz) || ld < d)
+        return fail(SGMV_ERR_INVALID, std::string(who) + ": " + name + " is required, aligned to its type, with a row stride >= d");
+    return SGMV_OK;
+}
+bool known_dtype(int32_t t) { return t == 0 || t == 1; }
+int64_t dtype_size(int32_t t) { return t == 0 ? 2 : 4; }
+
+// Blocks of a launch over `n` rows of `units` units each, `per` units a block.
+sgmv_status grid_of(const char* who, int64_t n, int64_t units, int64_t per, int32_t* chunks, unsigned* blocks) {
+    const int64_t c = (units + per - 1) / per;
+    if (n * c > INT32_MAX) return fail(SGMV_ERR_UNSUPPORTED, std::string(who) + ": T times the row length is too large for one launch");
+    *chunks = (int32_t)c;
+    *blocks = (unsigned)(n * c);
+    return SGMV_OK;
+}
+
+template <typename TI, typename TO>
+sgmv_status combine_typed(const char* who, const void* ys, int64_t ldys, int32_t rows, const int32_t* row_of,
+                          const float* w, int32_t T, int32_t k, int32_t d, const void* add, int64_t ldadd, void* y,
+                          int64_t ldy, cudaStream_t stream) {
+    const bool vec = d % 8 == 0 && rows16(ys, ldys, sizeof(TI)) && rows16(y, ldy, sizeof(TO)) &&
+                     (!add || rows16(add, ldadd, sizeof(TO)));
+    int32_t chunks;
+    unsigned blocks;
+    if (sgmv_status st = grid_of(who, T, vec ? d / 8 : d, kRowThreads, &chunks, &blocks); st != SGMV_OK) return st;
+    auto kern = vec ? combine_kernel<TI, TO, 8> : combine_kernel<TI, TO, 1>;
+    kern<<<blocks, kRowThreads, 0, stream>>>(static_cast<const TI*>(ys), ldys, rows, row_of, w, k, d, chunks,
+                                             static_cast<const TO*>(add), ldadd, static_cast<TO*>(y), ldy);
+    SGMV_CUDA_TRY(cudaGetLastError());
+    return SGMV_OK;
+}
+
+sgmv_status combine_impl(const char* who, const void* ys, int64_t ldys, int32_t rows, int32_t ys_dtype,
+                         const int32_t* row_of, const float* w, int32_t T, int32_t k, int32_t d, const void* add,
+                         int64_t ldadd, void* y, int64_t ldy, int32_t y_dtype, cudaStream_t stream) {
+    const std::string s(who);
+    sgmv_status st = check_rows(who, T, k, d, rows, row_of);
+    if (st != SGMV_OK) return st;
+    if (!known_dtype(ys_dtype) || !known_dtype(y_dtype))
+        return fail(SGMV_ERR_INVALID, s + ": a dtype must be 0 (bf16) or 1 (fp32)");
+    if (T == 0) return SGMV_OK;
+    if (rows > 0 && (st = check_matrix(who, "ys", ys, ldys, d, dtype_size(ys_dtype))) != SGMV_OK) return st;
+    if ((st = check_matrix(who, "y", y, ldy, d, dtype_size(y_dtype))) != SGMV_OK) return st;
+    if (add && (st = check_matrix(who, "add", add, ldadd, d, dtype_size(y_dtype))) != SGMV_OK) return st;
+    if (w && !aligned(w, 4)) return fail(SGMV_ERR_INVALID, s + ": weights must be 4-byte aligned");
+    auto run = ys_dtype == 0 ? (y_dtype == 0 ? combine_typed<uint16_t, uint16_t> : combine_typed<uint16_t, float>)
+                             : (y_dtype == 0 ? combine_typed<float, uint16_t> : combine_typed<float, float>);
+    return run(who, ys, ldys, rows, row_of, w, T, k, d, add, ldadd, y, ldy, stream);
+}
+
+template <typename TI, typename TO>
+sgmv_status combine_backward_typed(const void* dy, int64_t lddy, const void* ys, int64_t ldys, int32_t rows,
+                                   const int32_t* row_of, const float* w, int32_t T, int32_t k, int32_t d, void* dys,
+                                   int64_t lddys, float* dw, cudaStream_t stream) {
+    const bool vec = d % 8 == 0 && rows16(dy, lddy, sizeof(TO)) && (!dw || rows16(ys, ldys, sizeof(TI))) &&
+                     (!dys || rows16(dys, lddys, sizeof(TI)));
+    auto kern = vec ? combine_backward_kernel<TI, TO, 8> : combine_backward_kernel<TI, TO, 1>;
+    kern<<<(unsigned)(T * k), kRowThreads, 0, stream>>>(static_cast<const TO*>(dy), lddy, static_cast<const TI*>(ys),
+                                                        ldys, rows, row_of, w, k, d, static_cast<TI*>(dys), lddys, dw);
+    SGMV_CUDA_TRY(cudaGetLastError());
+    return SGMV_OK;
+}
+
+template <typename U>
+sgmv_status gather_typed(const void* x, int64_t ldx, int32_t T, int32_t units, const int32_t* row_of, int32_t k,
+                         void* xs, int64_t ldxs, int32_t rows, cudaStream_t stream) {
+    int32_t chunks;
+    unsigned blocks;
+    if (sgmv_status st = grid_of("expert_gather", T, units, 2 * kRowThreads, &chunks, &blocks); st != SGMV_OK) return st;
+    gather_kernel<U><<<blocks, kRowThreads, 0, stream>>>(static_cast<const U*>(x), ldx, units, chunks, row_of, k,
+                                                         static_cast<U*>(xs), ldxs, rows);
+    SGMV_CUDA_TRY(cudaGetLastError());
+    return SGMV_OK;
+}
+
+}  // namespace
+
+cudaError_t read_clear_errors_experts(uint32_t* bits, cudaStream_t stream) {
+    unsigned int h = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&h, g_err_experts, sizeof(h), 0, cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_err_experts, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    *bits |= h;
+    return e;
+}
+
+}  // namespace sgmv
+
+using namespace sgmv;
+
+extern "C" int64_t sgmv_expert_order_workspace(int32_t T, int32_t k, int32_t n_experts) {
+    if (T < 0 || k < 1 || k > kMaxExpertsPerToken || n_experts < 1 || n_experts > kMaxExperts) return -1;
+    if ((int64_t)T * k > kMaxSlots) return -1;
+    const int blocks = order_blocks((int64_t)T * k, n_experts);
+    return blocks == 1 ? 0 : (int64_t)blocks * n_experts * 4;
+}
+
+extern "C" sgmv_status sgmv_expert_order(const int32_t* expert_ids, int32_t T, int32_t k, int32_t n_experts,
+                                         int32_t* offsets, int32_t* row_of, int32_t* slot_of, void* workspace,
+                                         int64_t workspace_bytes, sgmv_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (T < 0) return fail(SGMV_ERR_INVALID, "expert_order: T >= 0 is required");
+    if (k < 1 || k > kMaxExpertsPerToken) return fail(SGMV_ERR_INVALID, "expert_order: k must be in 1..64");
+    if (n_experts < 1 || n_experts > kMaxExperts)
+        return fail(SGMV_ERR_INVALID, "expert_order: the number of experts must be in 1..4096");
+    const int64_t n = (int64_t)T * k;
+    if (n > kMaxSlots) return fail(SGMV_ERR_UNSUPPORTED, "expert_order: T * k must be at most 2^30");
+    if (!offsets || !aligned(offsets, 4) ||
+        (n > 0 && (!expert_ids || !row_of || !slot_of || !aligned(expert_ids, 4) || !aligned(row_of, 4) || !aligned(slot_of, 4))))
+        return fail(SGMV_ERR_INVALID, "expert_order: expert_ids, offsets, row_of and slot_of are required, 4-byte aligned");
+    const int blocks = order_blocks(n, n_experts), warps = order_warps(n_experts);
+    if (blocks > 1 && (!workspace || !aligned(workspace, 4))) return fail(SGMV_ERR_INVALID, "expert_order: a workspace is required, 4-byte aligned");
+    if (blocks > 1 && workspace_bytes < (int64_t)blocks * n_experts * 4)
+        return fail(SGMV_ERR_CAPACITY, "expert_order: the workspace is smaller than sgmv_expert_order_workspace says");
+    const int64_t tile = (n + blocks - 1) / blocks;
+    int32_t* counts = static_cast<int32_t*>(workspace);
+    const int smem = (warps * n_experts + n_experts + warps + 1) * 4;
+    if (smem > 48 * 1024)
+        SGMV_CUDA_TRY(cudaFuncSetAttribute(order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (blocks > 1) {
+        order_count_kernel<<<blocks, kOrderThreads, n_experts * 4, stream>>>(expert_ids, n, tile, n_experts, counts);
+        SGMV_CUDA_TRY(cudaGetLastError());
+    }
+    order_kernel<<<blocks, warps * 32, smem, stream>>>(expert_ids, n, tile, n_experts, counts, offsets, row_of, slot_of);
+    SGMV_CUDA_TRY(cudaGetLastError());
+    return SGMV_OK;
+}
+
+extern "C" sgmv_status sgmv_expert_gather(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t dtype,
+                                          const int32_t* row_of, int32_t k, void* xs, int64_t ldxs, int32_t rows,
+                                          sgmv_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    sgmv_status st = check_rows("expert_gather", T, k, d, rows, row_of);
+    if (st != SGMV_OK) return st;
+    if (!known_dtype(dtype)) return fail(SGMV_ERR_INVALID, "expert_gather: dtype must be 0 (bf16) or 1 (fp32)");
+    if (T == 0) return SGMV_OK;
+    const int64_t esz = dtype_size(dtype);
+    if ((st = check_matrix("expert_gather", "x", x, ldx, d, esz)) != SGMV_OK) return st;
+    if (rows > 0 && (st = check_matrix("expert_gather", "xs", xs, ldxs, d, esz)) != SGMV_OK) return st;
+    if (rows16(x, ldx, esz) && rows16(xs, ldxs, esz) && d * esz % 16 == 0)
+        return gather_typed<uint4>(x, ldx * esz / 16, T, (int32_t)(d * esz / 16), row_of, k, xs, ldxs * esz / 16, rows, stream);
+    return esz == 2 ? gather_typed<uint16_t>(x, ldx, T, d, row_of, k, xs, ldxs, rows, stream)
+                    : gather_typed<uint32_t>(x, ldx, T, d, row_of, k, xs, ldxs, rows, stream);
+}
+
+extern "C" sgmv_status sgmv_expert_gather_backward(const void* dxs, int64_t lddxs, int32_t rows, int32_t T, int32_t d,
+                                                   int32_t dtype, const int32_t* row_of, int32_t k, void* dx,
+                                                   int64_t lddx, sgmv_stream_t stream) {
+    return combine_impl("expert_gather_backward", dxs, lddxs, rows, dtype, row_of, nullptr, T, k, d, nullptr, 0, dx,
+                        lddx, dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" sgmv_status sgmv_expert_combine(const void* ys, int64_t ldys, int32_t rows, int32_t ys_dtype,
+                                           const int32_t* row_of, const float* weights, int32_t T, int32_t k, int32_t d,
+                                           const void* add, int64_t ldadd, void* y, int64_t ldy, int32_t y_dtype,
+                                           sgmv_stream_t stream) {
+    return combine_impl("expert_combine", ys, ldys, rows, ys_dtype, row_of, weights, T, k, d, add, ldadd, y, ldy,
+                        y_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" sgmv_status sgmv_expert_combine_backward(const void* dy, int64_t lddy, int32_t dy_dtype, const void* ys,
+                                                    int64_t ldys, int32_t rows, int32_t ys_dtype,
+                                                    const int32_t* row_of, const float* weights, int32_t T, int32_t k,
+                                                    int32_t d, void* dys, int64_t lddys, float* dweights,
+                                                    sgmv_stream_t stream_) {
+    const char* who = "expert_combine_backward";
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    sgmv_status st = check_rows(who, T, k, d, rows, row_of);
+    if (st != SGMV_OK) return st;
+    if (!known_dtype(dy_dtype) || !known_dtype(ys_dtype))
+        return fail(SGMV_ERR_INVALID, "expert_combine_backward: a dtype must be 0 (bf16) or 1 (fp32)");
+    if (T == 0 || (!dys && !dweights)) return SGMV_OK;
+    if ((st = check_matrix(who, "dy", dy, lddy, d, dtype_size(dy_dtype))) != SGMV_OK) return st;
+    if (dweights && rows > 0 && (st = check_matrix(who, "ys", ys, ldys, d, dtype_size(ys_dtype))) != SGMV_OK) return st;
+    if (dys && (st = check_matrix(who, "dys", dys, lddys, d, dtype_size(ys_dtype))) != SGMV_OK) return st;
+    if ((weights && !aligned(weights, 4)) || (dweights && !aligned(dweights, 4)))
+        return fail(SGMV_ERR_INVALID, "expert_combine_backward: weights and dweights must be 4-byte aligned");
+    auto run = ys_dtype == 0 ? (dy_dtype == 0 ? combine_backward_typed<uint16_t, uint16_t> : combine_backward_typed<uint16_t, float>)
+                             : (dy_dtype == 0 ? combine_backward_typed<float, uint16_t> : combine_backward_typed<float, float>);
+    return run(dy, lddy, ys, ldys, rows, row_of, weights, T, k, d, dys, lddys, dweights, stream);
+}
