@@ -607,7 +607,7 @@ SGMV_API sgmv_status sgmv_lora_delta_noalloc(const void* x, int64_t ldx, int32_t
  *          two's complement, -8..7; with zeros it is unsigned, 0..15.
  * scales   device [d_out][d_in / group], scale_dtype 0 = bf16, 1 = fp32
  * zeros    device uint8 [d_out][d_in / group], each 0..15, or NULL
- * group    32, 64 or 128 values; d_in is a multiple of it
+ * group    32, 64 or 128 values; d_in is a multiple of it, at most 524288
  * x        device bf16 [T][ldx], ldx >= d_in, row starts 16-byte aligned
  * y        device [T][ldy], ldy >= d_out, y_dtype 0 = bf16, 1 = fp32; aligned to
  *          its type.  It is written, not accumulated into, and may not overlap x.

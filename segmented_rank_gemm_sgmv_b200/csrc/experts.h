@@ -9,15 +9,17 @@
 namespace sgmv {
 
 constexpr int kMaxExperts = 4096;      // experts of one order / one base product
+constexpr int kMaxBaseK = 524288;      // d_in of a base product: x of one row fits into a cluster
 constexpr int kMaxExpertsPerToken = 64;
 constexpr int64_t kMaxSlots = 1 << 30; // token-expert slots of one order
 
 // Device error bit of these operators, beside those of ptx.cuh.
 enum : uint32_t { kErrExpert = 16u };  // expert id or expert offset out of range
 
-// Read and clear the device error words of the two translation units.
+// Read and clear the device error words of the translation units.
 cudaError_t read_clear_errors_experts(uint32_t* bits, cudaStream_t stream);
 cudaError_t read_clear_errors_base(uint32_t* bits, cudaStream_t stream);
+cudaError_t read_clear_errors_base_tc(uint32_t* bits, cudaStream_t stream);
 
 // y = W x for rows of 4-bit codes; see sgmv_base_product in include/sgmv.h.
 struct BaseArgs {
@@ -32,5 +34,8 @@ struct BaseArgs {
     const int32_t* slot_of;   // [rows] slot of each row (x row = slot / k), or null: x row = row
     int32_t rows, x_rows, k, experts, d_in, d_out, group;
 };
+
+// The tcgen05 kernel for many rows (sgmv_base_tc.cu); `per`: rows of a matrix, on average.
+cudaError_t launch_base_tc(const BaseArgs& a, int64_t per, bool scale_f32, bool y_f32, cudaStream_t stream);
 
 }  // namespace sgmv

@@ -1,0 +1,444 @@
+// Base products from 4-bit weights for many rows of x: tcgen05 tensor cores, fp32 accumulation per group.
+#include <algorithm>
+#include <cstring>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "experts.h"
+#include "ptx.cuh"
+
+namespace sgmv {
+
+__device__ unsigned int g_err_base_tc;
+
+namespace {
+
+// y^T = W x^T in tiles of 128 rows of W and NTOK rows of x.  tcgen05.mma takes the codes less their zero points,
+// exact in bf16, as its A operand and x as B, and sums one group of K values at a time into tensor memory; the
+// epilogue warps fetch each group's sums and add them, times the row's fp32 scale, to totals in registers, so that
+// no scale is ever rounded to bf16.  Two accumulators alternate between the groups.
+//
+// What bounds it: with 256 rows of x, the tensor cores (a group of 128 is 1024 cycles of MMA against about 600
+// issue slots of conversion and epilogue per scheduler); with few, the conversion of the codes, as in the kernel
+// for few rows, and the stream of codes.
+//
+// Roles (16 warps): 0 streams codes (TMA, stages of 128 rows x 256 values), 1 issues the MMAs, 2 and 3 copy x
+// (16-byte cp.async, so that rows may come from anywhere), kConvert warps turn codes into the A operand (a thread
+// a row), the rest are the epilogue.  K is split over the CTAs of a cluster when there are few tiles; their totals
+// meet in shared memory in a fixed order.
+template <int NTOK>
+struct TcConfig {
+    static constexpr int kConvert = NTOK <= 64 ? 8 : 4;              // warps
+    static constexpr int kEpilogue = 12 - kConvert;
+    static constexpr int kCols = NTOK / (kEpilogue / 4);             // columns of an epilogue warp
+    static constexpr int kStages = NTOK == 256 ? 3 : 4;              // of 64 K values
+    static constexpr int kCodeStages = 3;                            // of 256 K values
+    static constexpr int kA = 128 * 128, kB = NTOK * 128, kCodes = 128 * 128;
+    static constexpr int kSmem = 1024 + kStages * (kA + kB) + kCodeStages * kCodes;
+    static constexpr int kRedStride = 132;                           // floats of a row of x in the cluster's sum
+    static_assert(NTOK * kRedStride * 4 <= kSmem - 1024, "the totals fit into the operands' memory");
+};
+constexpr int kTcThreads = 512;
+constexpr int kTcRows = 128;
+
+enum : int { kTcDense = 0, kTcExperts = 1 };
+
+__device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst_smem)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Eight codes (value i in bits 4i..4i+3) less the zero point, as eight bf16 in order.  bf16 128 + n has the bits
+// 0x4300 | n for n < 128, so inserting the code and subtracting 128 + z is exact.  `flip` is 0x08080808 for two's
+// complement codes (n ^ 8 is the value plus 8; then z is 8).
+__device__ __forceinline__ uint4 convert8(uint32_t c, uint32_t flip, uint32_t z2) {
+    const uint32_t even = (c & 0x0f0f0f0fu) ^ flip, odd = ((c >> 4) & 0x0f0f0f0fu) ^ flip;
+    const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
+    uint32_t p[4] = {__byte_perm(lo, 0x43u, 0x4140), __byte_perm(lo, 0x43u, 0x4342), __byte_perm(hi, 0x43u, 0x4140),
+                     __byte_perm(hi, 0x43u, 0x4342)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&p[i]), *reinterpret_cast<const __nv_bfloat162*>(&z2));
+        p[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+    return make_uint4(p[0], p[1], p[2], p[3]);
+}
+
+template <int G, int NTOK, bool Z>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    base_tc_kernel(BaseArgs a, const __grid_constant__ CUtensorMap codes_map, bool scale_f32, bool y_f32, int n_split) {
+    using C = TcConfig<NTOK>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages], s_cfull[C::kCodeStages], s_cempty[C::kCodeStages],
+        s_afull[2], s_aempty[2], s_done;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_xrow[NTOK];
+    __shared__ int s_unit[3];
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int rank = blockIdx.x % n_split, n0 = (int)(blockIdx.x / n_split) * kTcRows;
+    uint8_t* stages = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;  // [kStages][A, B]
+    uint8_t* codes = stages + C::kStages * (C::kA + C::kB);                  // [kCodeStages]
+
+    // the unit: up to NTOK consecutive rows of y of one matrix
+    if (a.offsets) {
+        if (warp == 0) {                 // unit number blockIdx.y of the experts' units in order
+            int before = 0, found = 0, bad = 0;
+            for (int e0 = 0; e0 < a.experts && !found; e0 += 32) {
+                const int e = e0 + lane;
+                const int lo = e < a.experts ? a.offsets[e] : 0, hi = e < a.experts ? a.offsets[e + 1] : 0;
+                bad |= e < a.experts && (lo < 0 || hi < lo || hi > a.rows || (e == 0 && lo != 0));
+                const int first = max(lo, 0), end = min(hi, a.rows);
+                const int units = end > first ? (end - first + NTOK - 1) / NTOK : 0;
+                int upto = units;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += v;
+                }
+                const int k = (int)blockIdx.y - (before + upto - units);
+                if (k >= 0 && k < units) {
+                    s_unit[0] = e;
+                    s_unit[1] = first + k * NTOK;
+                    s_unit[2] = min(end, first + (k + 1) * NTOK);
+                }
+                found = __any_sync(0xffffffffu, k >= 0 && k < units);
+                before += __shfl_sync(0xffffffffu, upto, 31);
+            }
+            if (bad && blockIdx.x == 0) atomicOr(&g_err_base_tc, kErrExpert);
+            if (!found && lane == 0) s_unit[1] = s_unit[2] = s_unit[0] = 0;
+        }
+    } else if (tid == 0) {
+        s_unit[0] = 0;
+        s_unit[1] = blockIdx.y * NTOK;
+        s_unit[2] = min(a.rows, (int)(blockIdx.y + 1) * NTOK);
+    }
+    __syncthreads();
+    const int e = s_unit[0], row0 = s_unit[1], n_tok = s_unit[2] - row0;
+    if (n_tok <= 0) return;              // the same for every CTA of the cluster
+
+    // this CTA's code stages of K (256 values) and operand stages (64)
+    const int all = (a.d_in + 255) / 256;
+    const int c0 = (int)((int64_t)all * rank / n_split), c1 = (int)((int64_t)all * (rank + 1) / n_split);
+    const int k_begin = c0 * 256, k_end = min(a.d_in, c1 * 256), n_k = (k_end - k_begin + 63) / 64;
+    const int groups = a.d_in / G;
+
+    if (tid < NTOK) {
+        int r = -1;
+        if (tid < n_tok) {
+            r = row0 + tid;
+            if (a.slot_of) {
+                const int slot = a.slot_of[r];
+                r = slot >= 0 && slot / a.k < a.x_rows ? slot / a.k : -1;
+                if (r < 0) atomicOr(&g_err_base_tc, kErrRows);
+            }
+        }
+        s_xrow[tid] = r;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&s_full[i], 128 + 64);
+            mbar_init(&s_empty[i], 1);
+        }
+        for (int i = 0; i < C::kCodeStages; ++i) {
+            mbar_init(&s_cfull[i], 1);
+            mbar_init(&s_cempty[i], C::kConvert * 32);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_afull[i], 1);
+            mbar_init(&s_aempty[i], C::kEpilogue);
+        }
+        mbar_init(&s_done, 1);
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&s_tmem, 2 * NTOK);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    // waits give up together: whoever runs out of time stops the others' waits too
+    volatile int* abort_flag = &s_abort;
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!*abort_flag && !mbar_wait(bar, parity, &g_err_base_tc)) *abort_flag = 1;
+    };
+
+    float* red = reinterpret_cast<float*>(stages);                   // the CTA's totals, for its cluster
+
+    if (warp < 4) {
+        if constexpr (NTOK == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {
+            if (lane == 0) {
+                int i = 0;
+                for (; i < c1 - c0; ++i) {
+                    const int s = i % C::kCodeStages;
+                    if (i >= C::kCodeStages) wait(&s_cempty[s], (i / C::kCodeStages - 1) & 1);
+                    if (*abort_flag) break;
+                    mbar_arrive_expect_tx(&s_cfull[s], C::kCodes);
+                    tma_load_3d(codes + s * C::kCodes, &codes_map, (c0 + i) * 128, n0, e, &s_cfull[s]);
+                }
+                for (int j = max(0, i - C::kCodeStages); j < i; ++j)         // no copy is left in flight
+                    mbar_wait(&s_cfull[j % C::kCodeStages], (j / C::kCodeStages) & 1, &g_err_base_tc);
+            }
+        } else if (warp == 1) {
+            if (lane == 0) {
+                const uint32_t idesc = idesc_bf16_f32(128, NTOK, false, false);
+                int gi = 0;              // groups begun
+                for (int kt = 0; kt < n_k; ++kt) {
+                    const int s = kt % C::kStages;
+                    wait(&s_full[s], (kt / C::kStages) & 1);
+                    fence_proxy_async_smem();    // the operands were written through the generic proxy
+                    tc_fence_after();
+                    const uint32_t as = smem_u32(stages + s * (C::kA + C::kB)), bs = as + C::kA;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const int k = kt * 64 + ks * 16;
+                        if (k_begin + k >= k_end) break;
+                        if (k % G == 0) {
+                            if (gi >= 2) {
+                                wait(&s_aempty[gi % 2], (gi / 2 - 1) & 1);
+                                tc_fence_after();
+                            }
+                            ++gi;
+                        }
+                        const int buf = (gi - 1) % 2;
+                        tc_mma_bf16(tmem + buf * NTOK, smem_desc_sw128(as + ks * 32, 16, 1024), smem_desc_sw128(bs + ks * 32, 16, 1024),
+                                    idesc, k % G != 0);
+                        if ((k + 16) % G == 0) tc_commit(&s_afull[buf]);
+                    }
+                    tc_commit(&s_empty[s]);
+                }
+                tc_commit(&s_done);      // no MMA is left in flight
+                mbar_wait(&s_done, 0, &g_err_base_tc);
+            }
+        } else {
+            const int t = tid - 64, chunk = t % 8;
+            for (int kt = 0; kt < n_k; ++kt) {
+                const int s = kt % C::kStages;
+                if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
+                uint8_t* bs = stages + s * (C::kA + C::kB) + C::kA;
+                const int k = k_begin + kt * 64 + chunk * 8;
+#pragma unroll 8
+                for (int r = t / 8; r < NTOK; r += 8) {
+                    const int xr = s_xrow[r];
+                    const bool ok = xr >= 0 && k < k_end;
+                    cp_async16(bs + (r >> 3) * 1024 + sw128_off(r, chunk), a.x + (ok ? xr * a.ldx + k : 0), ok);
+                }
+                cp_async_mbar_arrive_noinc(&s_full[s]);
+            }
+            cp_async_wait<0>();
+        }
+        __syncwarp();
+    } else if (warp < 4 + C::kConvert) {
+        if constexpr (NTOK == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; with two parts they take alternate stages
+        constexpr int kParts = C::kConvert / 4;
+        constexpr int kZ = G >= 64 ? 1 : 2;                          // groups of a stage
+        const uint8_t* zrow = Z ? a.zeros + ((int64_t)e * a.d_out + min(n0 + r, a.d_out - 1)) * groups : nullptr;
+        uint32_t z_next[kZ] = {};
+        const auto load_zeros = [&](int kt) {
+            if constexpr (Z)
+#pragma unroll
+                for (int i = 0; i < kZ; ++i) z_next[i] = zrow[min((k_begin + kt * 64 + 32 * i) / G, groups - 1)];
+        };
+        load_zeros(part);
+        const uint32_t at = (r >> 3) * 1024 + (r & 7) * 128;
+        for (int kt = part; kt < n_k; kt += kParts) {
+            uint32_t z2[kZ];
+#pragma unroll
+            for (int i = 0; i < kZ; ++i) z2[i] = Z ? (0x4300u | z_next[i]) * 0x10001u : 0x43084308u;
+            load_zeros(kt + kParts);
+            const int s = kt % C::kStages, cs = kt / 4 % C::kCodeStages;
+            wait(&s_cfull[cs], (kt / 4 / C::kCodeStages) & 1);
+            if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
+            const uint8_t* cp = codes + cs * C::kCodes + at;
+            uint8_t* ap = stages + s * (C::kA + C::kB) + at;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 v = *reinterpret_cast<const uint4*>(cp + ((kt % 4 * 2 + h) ^ (r & 7)) * 16);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4*>(ap + ((4 * h + i) ^ (r & 7)) * 16) = convert8(w[i], Z ? 0u : 0x08080808u, z2[kZ == 1 ? 0 : h]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&s_full[s]);
+            if (kt % 4 / kParts == 4 / kParts - 1) mbar_arrive(&s_cempty[cs]);
+        }
+    } else {
+        if constexpr (NTOK == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int erow = (warp % 4) * 32 + lane, ecol = (warp - 4 - C::kConvert) / 4 * C::kCols;
+        float total[C::kCols];
+        const int64_t srow = ((int64_t)e * a.d_out + min(n0 + erow, a.d_out - 1)) * groups + k_begin / G;
+        const auto scale = [&](int g) {
+            return scale_f32 ? static_cast<const float*>(a.scales)[srow + g]
+                             : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.scales)[srow + g] << 16);
+        };
+#pragma unroll
+        for (int i = 0; i < C::kCols; ++i) total[i] = 0.0f;
+        const int n_g = (k_end - k_begin) / G;
+        float next = scale(0);
+        for (int g = 0; g < n_g; ++g) {
+            const float sc = next;
+            if (g + 1 < n_g) next = scale(g + 1);
+            const int buf = g % 2;
+            wait(&s_afull[buf], (g / 2) & 1);
+            tc_fence_after();
+            const uint32_t from = tmem + buf * NTOK + ecol + ((uint32_t)(warp % 4 * 32) << 16);
+            if constexpr (C::kCols % 32 == 0) {
+#pragma unroll
+                for (int c = 0; c < C::kCols; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(from + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) total[c + i] = fmaf(sc, __uint_as_float(v[i]), total[c + i]);
+                }
+            } else {
+                uint32_t v[16];
+                tmem_ld_x16(from, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) total[i] = fmaf(sc, __uint_as_float(v[i]), total[i]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_aempty[buf]);
+        }
+        if (n_split > 1) {               // the last group's MMAs are complete, and so are all before them
+#pragma unroll
+            for (int i = 0; i < C::kCols; ++i) red[(ecol + i) * C::kRedStride + erow] = total[i];
+        } else if (!*abort_flag && n0 + erow < a.d_out) {
+#pragma unroll
+            for (int i = 0; i < C::kCols; ++i)
+                if (ecol + i < n_tok && s_xrow[ecol + i] >= 0) {
+                    const int64_t to = (int64_t)(row0 + ecol + i) * a.ldy + n0 + erow;
+                    if (y_f32) static_cast<float*>(a.y)[to] = total[i];
+                    else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(total[i]));
+                }
+        }
+    }
+    __syncthreads();                     // every copy and MMA is complete: each was waited for
+    if (n_split > 1) {                   // the CTAs' totals, in a fixed order
+        cluster_sync();
+        const uint32_t base = smem_u32(red);
+        for (int i = rank * kTcThreads + tid; i < n_tok * 128; i += n_split * kTcThreads) {
+            const int t = i / 128, n = i % 128;
+            float v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = c < n_split ? ld_cluster_f32(map_cluster(base + (t * C::kRedStride + n) * 4, c)) : 0.0f;
+#pragma unroll
+            for (int c = 1; c < 8; ++c) v[0] += v[c];
+            if (n0 + n < a.d_out && s_xrow[t] >= 0 && !*abort_flag) {
+                const int64_t to = (int64_t)(row0 + t) * a.ldy + n0 + n;
+                if (y_f32) static_cast<float*>(a.y)[to] = v[0];
+                else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+            }
+        }
+        cluster_arrive_relaxed();        // every CTA of the cluster has read the totals
+        cluster_wait_acquire();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * NTOK);
+    }
+}
+
+// Tensor map over the codes, [experts][d_out][d_in / 2] bytes, for boxes of 128 rows of 128 bytes with the
+// 128-byte swizzle; what lies past a matrix's last row or a row's last byte reads as 0.
+cudaError_t encode_codes(CUtensorMap* map, const BaseArgs& a) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* f = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t row_bytes = a.d_in / 2;
+    const cuuint64_t dims[3] = {row_bytes, (cuuint64_t)a.d_out, (cuuint64_t)a.experts};
+    const cuuint64_t strides[2] = {row_bytes, row_bytes * a.d_out};
+    const cuuint32_t box[3] = {128, kTcRows, 1}, es[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a.codes), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+template <int G, int NTOK, bool Z>
+cudaError_t launch_t(const BaseArgs& a, bool scale_f32, bool y_f32, cudaStream_t stream) {
+    using C = TcConfig<NTOK>;
+    auto kern = base_tc_kernel<G, NTOK, Z>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (err != cudaSuccess) return err;
+    CUtensorMap map;
+    if ((err = encode_codes(&map, a)) != cudaSuccess) return err;
+    const int tiles = (a.d_out + kTcRows - 1) / kTcRows, k_stages = (a.d_in + 255) / 256;
+    const int64_t units = a.offsets ? (int64_t)a.rows / NTOK + std::min(a.rows, a.experts) : ((int64_t)a.rows + NTOK - 1) / NTOK;
+    int split = 1;
+    if (!a.offsets)
+        while (split < 8 && 4 * split <= k_stages && tiles * units * split < 148) split *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)units);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a, map, scale_f32, y_f32, split);
+}
+
+template <int G, bool Z>
+cudaError_t launch_g(const BaseArgs& a, int64_t per, bool scale_f32, bool y_f32, cudaStream_t stream) {
+    if (per <= 32) return launch_t<G, 32, Z>(a, scale_f32, y_f32, stream);
+    if (per <= 64) return launch_t<G, 64, Z>(a, scale_f32, y_f32, stream);
+    if (per <= 128) return launch_t<G, 128, Z>(a, scale_f32, y_f32, stream);
+    return launch_t<G, 256, Z>(a, scale_f32, y_f32, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_base_tc(const BaseArgs& a, int64_t per, bool scale_f32, bool y_f32, cudaStream_t stream) {
+    if (a.zeros)
+        return a.group == 128  ? launch_g<128, true>(a, per, scale_f32, y_f32, stream)
+               : a.group == 64 ? launch_g<64, true>(a, per, scale_f32, y_f32, stream)
+                               : launch_g<32, true>(a, per, scale_f32, y_f32, stream);
+    return a.group == 128  ? launch_g<128, false>(a, per, scale_f32, y_f32, stream)
+           : a.group == 64 ? launch_g<64, false>(a, per, scale_f32, y_f32, stream)
+                           : launch_g<32, false>(a, per, scale_f32, y_f32, stream);
+}
+
+cudaError_t read_clear_errors_base_tc(uint32_t* bits, cudaStream_t stream) {
+    unsigned int h = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&h, g_err_base_tc, sizeof(h), 0, cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_err_base_tc, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    *bits |= h;
+    return e;
+}
+
+}  // namespace sgmv

@@ -37,7 +37,7 @@ def experts(**kw):
 
 
 @pytest.mark.parametrize("kw", [dict(E=0), dict(E=4097), dict(offsets=None), dict(offsets=P + 2), dict(x_rows=3), dict(slot_of=P, k=0),
-                                dict(slot_of=P, k=65), dict(slot_of=P + 1), dict(rows=-1), dict(x_rows=-1)])
+                                dict(slot_of=P, k=65), dict(slot_of=P, x_rows=0), dict(slot_of=P + 1), dict(rows=-1), dict(x_rows=-1)])
 def test_base_product_experts_refuses(kw):
     assert experts(**kw) == 1 and b"base_product_experts" in sg.load_library().sgmv_last_error()
 
