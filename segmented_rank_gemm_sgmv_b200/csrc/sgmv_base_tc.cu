@@ -23,8 +23,8 @@ namespace {
 // issue slots of conversion and epilogue per scheduler); with few, the conversion of the codes, as in the kernel
 // for few rows, and the stream of codes.
 //
-// Roles (16 warps): 0 streams codes (TMA, stages of 128 rows x 256 values), 1 issues the MMAs, 2 and 3 copy x
-// (16-byte cp.async, so that rows may come from anywhere), kConvert warps turn codes into the A operand (a thread
+// Roles (16 warps): 0 streams codes (TMA, stages of 128 rows x 256 values), 1 issues the MMAs, 2 copies x (TMA: one
+// tiled load a stage, or loads of four rows each where the rows are not consecutive), kConvert warps turn codes into the A operand (a thread
 // a row), the rest are the epilogue.  K is split over the CTAs of a cluster when there are few tiles; their totals
 // meet in shared memory in a fixed order.
 template <int NTOK>
@@ -51,12 +51,39 @@ __device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* map, int
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+// Four rows of a 2-D map whose box is one row high, to consecutive rows in shared memory.
+__device__ __forceinline__ void tma_gather4(void* dst_smem, const void* map, int x, int4 rows, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            smem_u32(dst_smem)),
+        "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(smem_u32(bar))
+        : "memory");
+}
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+
+// tc_mma_bf16 and tc_commit by one lane of a converged warp.  The election is inside, so that the operands stay in
+// uniform registers; under a branch on the lane each MMA took about 200 cycles to issue.
+__device__ __forceinline__ void mma_elected(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
 }
 
 // Eight codes (value i in bits 4i..4i+3) less the zero point, as eight bf16 in order.  bf16 128 + n has the bits
@@ -77,16 +104,17 @@ __device__ __forceinline__ uint4 convert8(uint32_t c, uint32_t flip, uint32_t z2
 
 template <int G, int NTOK, bool Z>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    base_tc_kernel(BaseArgs a, const __grid_constant__ CUtensorMap codes_map, bool scale_f32, bool y_f32, int n_split) {
+    base_tc_kernel(BaseArgs a, const __grid_constant__ CUtensorMap codes_map,
+                   const __grid_constant__ CUtensorMap x_map, bool scale_f32, bool y_f32, int n_split) {
     using C = TcConfig<NTOK>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages], s_cfull[C::kCodeStages], s_cempty[C::kCodeStages],
         s_afull[2], s_aempty[2], s_done;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_xrow[NTOK];
+    __shared__ __align__(16) int s_xrow[NTOK];                       // rows of x; one past the last where there is none
     __shared__ int s_unit[3];
     __shared__ int s_abort;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
     const int rank = blockIdx.x % n_split, n0 = (int)(blockIdx.x / n_split) * kTcRows;
     uint8_t* stages = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;  // [kStages][A, B]
     uint8_t* codes = stages + C::kStages * (C::kA + C::kB);                  // [kCodeStages]
@@ -135,20 +163,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int groups = a.d_in / G;
 
     if (tid < NTOK) {
-        int r = -1;
+        int r = a.x_rows;
         if (tid < n_tok) {
             r = row0 + tid;
             if (a.slot_of) {
                 const int slot = a.slot_of[r];
-                r = slot >= 0 && slot / a.k < a.x_rows ? slot / a.k : -1;
-                if (r < 0) atomicOr(&g_err_base_tc, kErrRows);
+                r = slot >= 0 && slot / a.k < a.x_rows ? slot / a.k : a.x_rows;
+                if (r == a.x_rows) atomicOr(&g_err_base_tc, kErrRows);
             }
         }
         s_xrow[tid] = r;
     }
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&s_full[i], 128 + 64);
+            mbar_init(&s_full[i], 128 + 1);
             mbar_init(&s_empty[i], 1);
         }
         for (int i = 0; i < C::kCodeStages; ++i) {
@@ -170,7 +198,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     // waits give up together: whoever runs out of time stops the others' waits too
     volatile int* abort_flag = &s_abort;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -179,6 +207,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     float* red = reinterpret_cast<float*>(stages);                   // the CTA's totals, for its cluster
 
+    int n_x = 0;                         // stages of x asked for
     if (warp < 4) {
         if constexpr (NTOK == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
@@ -195,52 +224,54 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_wait(&s_cfull[j % C::kCodeStages], (j / C::kCodeStages) & 1, &g_err_base_tc);
             }
         } else if (warp == 1) {
-            if (lane == 0) {
-                const uint32_t idesc = idesc_bf16_f32(128, NTOK, false, false);
-                int gi = 0;              // groups begun
-                for (int kt = 0; kt < n_k; ++kt) {
-                    const int s = kt % C::kStages;
-                    wait(&s_full[s], (kt / C::kStages) & 1);
-                    fence_proxy_async_smem();    // the operands were written through the generic proxy
-                    tc_fence_after();
-                    const uint32_t as = smem_u32(stages + s * (C::kA + C::kB)), bs = as + C::kA;
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        const int k = kt * 64 + ks * 16;
-                        if (k_begin + k >= k_end) break;
-                        if (k % G == 0) {
-                            if (gi >= 2) {
-                                wait(&s_aempty[gi % 2], (gi / 2 - 1) & 1);
-                                tc_fence_after();
-                            }
-                            ++gi;
-                        }
-                        const int buf = (gi - 1) % 2;
-                        tc_mma_bf16(tmem + buf * NTOK, smem_desc_sw128(as + ks * 32, 16, 1024), smem_desc_sw128(bs + ks * 32, 16, 1024),
-                                    idesc, k % G != 0);
-                        if ((k + 16) % G == 0) tc_commit(&s_afull[buf]);
-                    }
-                    tc_commit(&s_empty[s]);
-                }
-                tc_commit(&s_done);      // no MMA is left in flight
-                mbar_wait(&s_done, 0, &g_err_base_tc);
-            }
-        } else {
-            const int t = tid - 64, chunk = t % 8;
+            const uint32_t idesc = idesc_bf16_f32(128, NTOK, false, false);
+            const uint64_t adesc = smem_desc_sw128(smem_u32(stages), 16, 1024), bdesc = smem_desc_sw128(smem_u32(stages) + C::kA, 16, 1024);
+            int gi = 0;                  // groups begun
+            int s = 0, buf = 0;
             for (int kt = 0; kt < n_k; ++kt) {
+                wait(&s_full[s], (kt / C::kStages) & 1);
+                tc_fence_after();
+                const uint64_t at = (uint64_t)(s * ((C::kA + C::kB) / 16));
+                const int steps = min(4, (k_end - k_begin - kt * 64) / 16);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    if (ks >= steps) break;
+                    const bool first = G == 128 ? ks == 0 && kt % 2 == 0 : G == 64 ? ks == 0 : ks % 2 == 0;
+                    const bool last = G == 128 ? ks == 3 && kt % 2 == 1 : G == 64 ? ks == 3 : ks % 2 == 1;
+                    if (first) {
+                        if (gi >= 2) {
+                            wait(&s_aempty[gi % 2], (gi / 2 - 1) & 1);
+                            tc_fence_after();
+                        }
+                        buf = gi++ % 2;
+                    }
+                    mma_elected(tmem + buf * NTOK, adesc + at + ks * 2, bdesc + at + ks * 2, idesc, !first);
+                    if (last) commit_elected(&s_afull[buf]);
+                }
+                commit_elected(&s_empty[s]);
+                s = s == C::kStages - 1 ? 0 : s + 1;
+            }
+            commit_elected(&s_done);     // no MMA is left in flight
+            mbar_wait(&s_done, 0, &g_err_base_tc);
+        } else {
+            // x: consecutive rows by one tiled load a stage, else four rows a load; rows that do not exist read as 0
+            for (int kt = 0; warp == 2 && kt < n_k; ++kt) {
                 const int s = kt % C::kStages;
                 if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
+                if (*abort_flag) break;
                 uint8_t* bs = stages + s * (C::kA + C::kB) + C::kA;
-                const int k = k_begin + kt * 64 + chunk * 8;
-#pragma unroll 8
-                for (int r = t / 8; r < NTOK; r += 8) {
-                    const int xr = s_xrow[r];
-                    const bool ok = xr >= 0 && k < k_end;
-                    cp_async16(bs + (r >> 3) * 1024 + sw128_off(r, chunk), a.x + (ok ? xr * a.ldx + k : 0), ok);
+                if (lane == 0) mbar_arrive_expect_tx(&s_full[s], C::kB);
+                __syncwarp();
+                if (!a.slot_of) {
+                    if (lane == 0) tma_load_2d(bs, &x_map, k_begin + kt * 64, row0, &s_full[s]);
+                } else {
+#pragma unroll
+                    for (int r = lane * 4; r < NTOK; r += 128) tma_gather4(bs + r * 128, &x_map, k_begin + kt * 64, *reinterpret_cast<const int4*>(&s_xrow[r]), &s_full[s]);
                 }
-                cp_async_mbar_arrive_noinc(&s_full[s]);
+                n_x = kt + 1;
             }
-            cp_async_wait<0>();
+            if (*abort_flag)             // no copy is left in flight
+                for (int kt = max(0, n_x - C::kStages); kt < n_x; ++kt) mbar_wait(&s_full[kt % C::kStages], (kt / C::kStages) & 1, &g_err_base_tc);
         }
         __syncwarp();
     } else if (warp < 4 + C::kConvert) {
@@ -325,7 +356,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         } else if (!*abort_flag && n0 + erow < a.d_out) {
 #pragma unroll
             for (int i = 0; i < C::kCols; ++i)
-                if (ecol + i < n_tok && s_xrow[ecol + i] >= 0) {
+                if (ecol + i < n_tok && s_xrow[ecol + i] < a.x_rows) {
                     const int64_t to = (int64_t)(row0 + ecol + i) * a.ldy + n0 + erow;
                     if (y_f32) static_cast<float*>(a.y)[to] = total[i];
                     else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(total[i]));
@@ -343,7 +374,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int c = 0; c < 8; ++c) v[c] = c < n_split ? ld_cluster_f32(map_cluster(base + (t * C::kRedStride + n) * 4, c)) : 0.0f;
 #pragma unroll
             for (int c = 1; c < 8; ++c) v[0] += v[c];
-            if (n0 + n < a.d_out && s_xrow[t] >= 0 && !*abort_flag) {
+            if (n0 + n < a.d_out && s_xrow[t] < a.x_rows && !*abort_flag) {
                 const int64_t to = (int64_t)(row0 + t) * a.ldy + n0 + n;
                 if (y_f32) static_cast<float*>(a.y)[to] = v[0];
                 else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
@@ -358,9 +389,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
-// Tensor map over the codes, [experts][d_out][d_in / 2] bytes, for boxes of 128 rows of 128 bytes with the
-// 128-byte swizzle; what lies past a matrix's last row or a row's last byte reads as 0.
-cudaError_t encode_codes(CUtensorMap* map, const BaseArgs& a) {
+// A tensor map with the 128-byte swizzle; what lies past an end reads as 0.
+cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box) {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         cudaDriverEntryPointQueryResult q;
         void* f = nullptr;
@@ -369,14 +400,24 @@ cudaError_t encode_codes(CUtensorMap* map, const BaseArgs& a) {
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     }();
     if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t row_bytes = a.d_in / 2;
-    const cuuint64_t dims[3] = {row_bytes, (cuuint64_t)a.d_out, (cuuint64_t)a.experts};
-    const cuuint64_t strides[2] = {row_bytes, row_bytes * a.d_out};
-    const cuuint32_t box[3] = {128, kTcRows, 1}, es[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a.codes), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(map, type, rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
+}
+// The codes, [experts][d_out][d_in / 2] bytes, in boxes of 128 rows of 128 bytes.
+cudaError_t encode_codes(CUtensorMap* map, const BaseArgs& a) {
+    const cuuint64_t row_bytes = a.d_in / 2;
+    const cuuint64_t dims[3] = {row_bytes, (cuuint64_t)a.d_out, (cuuint64_t)a.experts}, strides[2] = {row_bytes, row_bytes * a.d_out};
+    const cuuint32_t box[3] = {128, kTcRows, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.codes, dims, strides, box);
+}
+// x in boxes of 64 values of `rows` rows (1 for loads of four rows of any place).
+cudaError_t encode_x(CUtensorMap* map, const BaseArgs& a, int rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)a.d_in, (cuuint64_t)a.x_rows}, strides[1] = {(cuuint64_t)a.ldx * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)rows};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, dims, strides, box);
 }
 
 template <int G, int NTOK, bool Z>
@@ -385,8 +426,8 @@ cudaError_t launch_t(const BaseArgs& a, bool scale_f32, bool y_f32, cudaStream_t
     auto kern = base_tc_kernel<G, NTOK, Z>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (err != cudaSuccess) return err;
-    CUtensorMap map;
-    if ((err = encode_codes(&map, a)) != cudaSuccess) return err;
+    CUtensorMap map, x_map;
+    if ((err = encode_codes(&map, a)) != cudaSuccess || (err = encode_x(&x_map, a, a.slot_of ? 1 : NTOK)) != cudaSuccess) return err;
     const int tiles = (a.d_out + kTcRows - 1) / kTcRows, k_stages = (a.d_in + 255) / 256;
     const int64_t units = a.offsets ? (int64_t)a.rows / NTOK + std::min(a.rows, a.experts) : ((int64_t)a.rows + NTOK - 1) / NTOK;
     int split = 1;
@@ -404,7 +445,7 @@ cudaError_t launch_t(const BaseArgs& a, bool scale_f32, bool y_f32, cudaStream_t
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, a, map, scale_f32, y_f32, split);
+    return cudaLaunchKernelEx(&cfg, kern, a, map, x_map, scale_f32, y_f32, split);
 }
 
 template <int G, bool Z>
