@@ -628,6 +628,9 @@ SGMV_API sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, in
  * offsets  device int32 [n_experts + 1], ascending from 0, last <= rows
  * slot_of  device int32 [rows] (sgmv_expert_order), or NULL; k: choices per token
  * rows     rows of y; x_rows: rows of x (>= rows without slot_of)
+ * workspace device, 16-byte aligned, for calls with slot_of: the bytes that
+ *          sgmv_base_product_experts_workspace gives (0: may be NULL); nothing in
+ *          it is kept, but two calls that may overlap need two
  * Rows of y from offsets[n_experts] on are left as they were.  A slot whose
  * token is not a row of x is reported by sgmv_check_errors and its row left
  * unwritten; offsets that do not ascend from 0 to at most rows are reported, and
@@ -638,7 +641,9 @@ SGMV_API sgmv_status sgmv_base_product_experts(const void* x, int64_t ldx, int32
                                                const void* scales, int32_t scale_dtype, const uint8_t* zeros,
                                                int32_t group, const int32_t* offsets, const int32_t* slot_of,
                                                int32_t k, int32_t rows, void* y, int64_t ldy, int32_t y_dtype,
-                                               sgmv_stream_t stream);
+                                               void* workspace, int64_t workspace_bytes, sgmv_stream_t stream);
+/* Bytes of workspace of a call with slot_of (0: none; -1: refused sizes). */
+SGMV_API int64_t sgmv_base_product_experts_workspace(int32_t rows, int32_t d_in, int32_t n_experts);
 
 /* ------------------------------------------------------------------------ */
 /* Tokens sorted by expert and back                                          */

@@ -40,6 +40,7 @@ EXPORTED = ("sgmv_status_string", "sgmv_last_error", "sgmv_pool_create", "sgmv_p
             "sgmv_check_errors", "sgmv_residency_create", "sgmv_residency_destroy",
             "sgmv_residency_register", "sgmv_residency_unregister", "sgmv_residency_prepare",
             "sgmv_residency_get_stats", "sgmv_base_product", "sgmv_base_product_experts",
+            "sgmv_base_product_experts_workspace",
             "sgmv_expert_order_workspace", "sgmv_expert_order", "sgmv_expert_gather", "sgmv_expert_gather_backward",
             "sgmv_expert_combine", "sgmv_expert_combine_backward")
 
@@ -140,7 +141,8 @@ def load_library() -> ctypes.CDLL:
         "sgmv_residency_get_stats": (st, [vp, ctypes.POINTER(ResidencyStats)]),
         "sgmv_base_product": (st, [vp, i64, i32, i32, i32, vp, vp, i32, vp, i32, vp, i64, i32, vp]),
         "sgmv_base_product_experts": (st, [vp, i64, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, i32, i32, vp,
-                                           i64, i32, vp]),
+                                           i64, i32, vp, i64, vp]),
+        "sgmv_base_product_experts_workspace": (i64, [i32, i32, i32]),
         "sgmv_expert_order_workspace": (i64, [i32, i32, i32]),
         "sgmv_expert_order": (st, [vp, i32, i32, i32, vp, vp, vp, vp, i64, vp]),
         "sgmv_expert_gather": (st, [vp, i64, i32, i32, i32, vp, i32, vp, i64, i32, vp]),
@@ -710,6 +712,14 @@ def _here(t: torch.Tensor, name: str):
     return d
 
 
+def _record(made, stream) -> None:
+    """Tensors made by a call that runs on `stream`: their memory is reused only after it."""
+    if stream is not None and made:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        for t in made:
+            t.record_stream(s)
+
+
 def _weights4(codes, scales, zeros, lead: int, device):
     """Checks and addresses of a 4-bit matrix: codes [.., d_out, d_in / 2], scales and zeros [.., d_out, d_in / group]."""
     pc = _flat(codes, "codes", torch.uint8, device)
@@ -760,16 +770,22 @@ def base_product_experts(x: torch.Tensor, codes: torch.Tensor, scales: torch.Ten
     _need(y.shape[1] == d_out, "y must be [rows, d_out]")
     po = _flat(offsets, "offsets", torch.int32, dev)
     _need(offsets.numel() == n_experts + 1, "offsets must have one value per expert and one more")
-    psl, k = None, 1
+    lib = load_library()
+    psl, k, pw, need = None, 1, None, 0
     if slot_of is not None:
         psl = _flat(slot_of, "slot_of", torch.int32, dev)
         _need(slot_of.numel() == rows and (rows % x_rows == 0 if x_rows else rows == 0),
               "slot_of must have a slot for every row of y, k for every row of x")
         k = rows // x_rows if rows else 1
+        need = lib.sgmv_base_product_experts_workspace(rows, d_in, n_experts)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            pw = workspace.data_ptr()
+            _record([workspace], stream)
     else:
         _need(x_rows == rows, "x and y must have the same rows without slot_of")
-    _check(load_library().sgmv_base_product_experts(px, ldx, x_rows, d_in, d_out, n_experts, pc, ps, sdt, pz, group, po,
-                                                    psl, k, rows, py, ldy, _DTYPE[y.dtype], _stream(stream)))
+    _check(lib.sgmv_base_product_experts(px, ldx, x_rows, d_in, d_out, n_experts, pc, ps, sdt, pz, group, po, psl, k, rows,
+                                         py, ldy, _DTYPE[y.dtype], pw, max(need, 0), _stream(stream)))
     return y
 
 
@@ -800,10 +816,7 @@ def expert_order(expert_ids: torch.Tensor, n_experts: int, offsets: Optional[tor
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         made.append(workspace)
-    if stream is not None and made:      # their memory may be reused by the current stream only after `stream`
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        for t in made:
-            t.record_stream(s)
+    _record(made, stream)
     pw, nw = (None, 0) if workspace is None else (_flat(workspace, "workspace", workspace.dtype, dev),
                                                   workspace.numel() * workspace.element_size())
     _check(lib.sgmv_expert_order(pi, T, k, n_experts, _flat(offsets, "offsets", torch.int32, dev),

@@ -468,10 +468,34 @@ cudaError_t launch_rows(const BaseArgs& a, int64_t per, bool scale_f32, bool y_f
     return per <= 8 ? launch_rows_z<G, 1>(a, scale_f32, y_f32, stream) : launch_rows_z<G, 2>(a, scale_f32, y_f32, stream);
 }
 
-cudaError_t launch_product(const BaseArgs& a, bool scale_f32, bool y_f32, cudaStream_t stream) {
-    // rows of a matrix, on average: from 17 on the tensor-core kernel is the faster
-    const int64_t per = a.offsets ? ((int64_t)a.rows + a.experts - 1) / a.experts : a.rows;
-    if (per > 16) return launch_base_tc(a, per, scale_f32, y_f32, stream);
+// Rows of a matrix, on average.
+int64_t rows_each(int64_t rows, int64_t experts) { return (rows + experts - 1) / experts; }
+// From this many rows a matrix on, the tensor-core kernel is the faster.
+constexpr int kTcFrom = 17;
+
+// Rows slot_of[r] / k of x to rows r of a workspace, for the tensor-core kernel, whose copies of x take consecutive
+// rows (four rows a copy, from anywhere, took 2.5 times as long as this and the product together).
+__global__ void __launch_bounds__(256) base_gather_kernel(BaseArgs a, uint4* to) {
+    const int units = a.d_in / 8, r = blockIdx.x, slot = a.slot_of[r];
+    if (slot < 0 || slot / a.k >= a.x_rows) {
+        if (threadIdx.x == 0 && r < a.offsets[a.experts]) atomicOr(&g_err_base, kErrRows);
+        return;
+    }
+    const uint4* from = reinterpret_cast<const uint4*>(a.x + (int64_t)(slot / a.k) * a.ldx);
+    for (int i = threadIdx.x; i < units; i += 256) to[(int64_t)r * units + i] = from[i];
+}
+
+cudaError_t launch_product(BaseArgs a, bool scale_f32, bool y_f32, void* workspace, cudaStream_t stream) {
+    const int64_t per = a.offsets ? rows_each(a.rows, a.experts) : a.rows;
+    if (per >= kTcFrom) {
+        if (a.slot_of) {
+            base_gather_kernel<<<a.rows, 256, 0, stream>>>(a, static_cast<uint4*>(workspace));
+            if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+            a.x = static_cast<const uint16_t*>(workspace);
+            a.ldx = a.d_in;
+        }
+        return launch_base_tc(a, per, scale_f32, y_f32, stream);
+    }
     return a.group == 128  ? launch_rows<128>(a, per, scale_f32, y_f32, stream)
            : a.group == 64 ? launch_rows<64>(a, per, scale_f32, y_f32, stream)
                            : launch_rows<32>(a, per, scale_f32, y_f32, stream);
@@ -479,7 +503,7 @@ cudaError_t launch_product(const BaseArgs& a, bool scale_f32, bool y_f32, cudaSt
 
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 
-sgmv_status product_impl(const char* who_, BaseArgs a, int32_t scale_dtype, int32_t y_dtype, cudaStream_t stream) {
+sgmv_status product_impl(const char* who_, const BaseArgs& a, int32_t scale_dtype, int32_t y_dtype, void* workspace, cudaStream_t stream) {
     const std::string who(who_);
     if (a.rows < 0 || a.x_rows < 0 || a.d_in < 1 || a.d_out < 1)
         return fail(SGMV_ERR_INVALID, who + ": the numbers of rows must be >= 0, d_in and d_out >= 1");
@@ -497,7 +521,7 @@ sgmv_status product_impl(const char* who_, BaseArgs a, int32_t scale_dtype, int3
     if (!aligned(a.scales, scale_dtype ? 4 : 2)) return fail(SGMV_ERR_INVALID, who + ": scales must be aligned to their type");
     if (a.ldy < a.d_out || !aligned(a.y, y_dtype ? 4 : 2))
         return fail(SGMV_ERR_INVALID, who + ": y must be aligned to its type, ldy >= d_out");
-    SGMV_CUDA_TRY(launch_product(a, scale_dtype == 1, y_dtype == 1, stream));
+    SGMV_CUDA_TRY(launch_product(a, scale_dtype == 1, y_dtype == 1, workspace, stream));
     return SGMV_OK;
 }
 
@@ -527,7 +551,12 @@ extern "C" sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, 
                                          sgmv_stream_t stream) {
     const BaseArgs a{static_cast<const uint16_t*>(x), ldx, static_cast<const uint8_t*>(codes), scales, zeros, y, ldy,
                      nullptr, nullptr, T, T, 1, 1, d_in, d_out, group};
-    return product_impl("base_product", a, scale_dtype, y_dtype, reinterpret_cast<cudaStream_t>(stream));
+    return product_impl("base_product", a, scale_dtype, y_dtype, nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int64_t sgmv_base_product_experts_workspace(int32_t rows, int32_t d_in, int32_t n_experts) {
+    if (rows < 0 || d_in < 1 || n_experts < 1 || n_experts > kMaxExperts) return -1;
+    return rows_each(rows, n_experts) >= kTcFrom ? (int64_t)rows * d_in * 2 : 0;
 }
 
 extern "C" sgmv_status sgmv_base_product_experts(const void* x, int64_t ldx, int32_t x_rows, int32_t d_in,
@@ -535,7 +564,7 @@ extern "C" sgmv_status sgmv_base_product_experts(const void* x, int64_t ldx, int
                                                  const void* scales, int32_t scale_dtype, const uint8_t* zeros,
                                                  int32_t group, const int32_t* offsets, const int32_t* slot_of,
                                                  int32_t k, int32_t rows, void* y, int64_t ldy, int32_t y_dtype,
-                                                 sgmv_stream_t stream) {
+                                                 void* workspace, int64_t workspace_bytes, sgmv_stream_t stream) {
     const char* who = "base_product_experts";
     if (n_experts < 1 || n_experts > kMaxExperts)
         return fail(SGMV_ERR_INVALID, "base_product_experts: the number of experts must be in 1..4096");
@@ -545,5 +574,10 @@ extern "C" sgmv_status sgmv_base_product_experts(const void* x, int64_t ldx, int
         return fail(SGMV_ERR_INVALID, "base_product_experts: slot_of needs k in 1..64 and a row of x; without it x has a row for every row of y");
     const BaseArgs a{static_cast<const uint16_t*>(x), ldx, static_cast<const uint8_t*>(codes), scales, zeros, y, ldy,
                      offsets, slot_of, rows, x_rows, slot_of ? k : 1, n_experts, d_in, d_out, group};
-    return product_impl(who, a, scale_dtype, y_dtype, reinterpret_cast<cudaStream_t>(stream));
+    const int64_t need = slot_of ? sgmv_base_product_experts_workspace(rows, d_in, n_experts) : 0;
+    if (need > 0 && (!workspace || !aligned(workspace, 16)))
+        return fail(SGMV_ERR_INVALID, "base_product_experts: a workspace is required, 16-byte aligned");
+    if (need > workspace_bytes)
+        return fail(SGMV_ERR_CAPACITY, "base_product_experts: the workspace is smaller than sgmv_base_product_experts_workspace says");
+    return product_impl(who, a, scale_dtype, y_dtype, workspace, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -23,40 +23,30 @@ namespace {
 // issue slots of conversion and epilogue per scheduler); with few, the conversion of the codes, as in the kernel
 // for few rows, and the stream of codes.
 //
-// Roles (16 warps): 0 streams codes (TMA, stages of 128 rows x 256 values), 1 issues the MMAs, 2 copies x (TMA: one
-// tiled load a stage, or loads of four rows each where the rows are not consecutive), kConvert warps turn codes into the A operand (a thread
-// a row), the rest are the epilogue.  K is split over the CTAs of a cluster when there are few tiles; their totals
-// meet in shared memory in a fixed order.
+// Roles: warp 0 streams codes (TMA, stages of 128 rows x 256 values), 1 issues the MMAs, 2 copies x (TMA), 8 warps
+// turn codes into the A operand (a thread a row, half of the warps each stage), the rest are the epilogue.  K is
+// split over the CTAs of a cluster when there are few tiles; their totals meet in shared memory in a fixed order.
 template <int NTOK>
 struct TcConfig {
-    static constexpr int kConvert = NTOK <= 64 ? 8 : 4;              // warps
-    static constexpr int kEpilogue = 12 - kConvert;
+    static constexpr int kConvert = 8;                               // warps
+    static constexpr int kEpilogue = NTOK <= 64 ? 4 : 8;
+    static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
     static constexpr int kCols = NTOK / (kEpilogue / 4);             // columns of an epilogue warp
-    static constexpr int kStages = NTOK == 256 ? 3 : 4;              // of 64 K values
+    static constexpr int kStageK = NTOK <= 64 ? 128 : 64;            // K values of an operand stage
+    static constexpr int kStages = NTOK == 128 ? 4 : 3;
     static constexpr int kCodeStages = 3;                            // of 256 K values
-    static constexpr int kA = 128 * 128, kB = NTOK * 128, kCodes = 128 * 128;
+    static constexpr int kA = 128 * 2 * kStageK, kB = NTOK * 2 * kStageK, kCodes = 128 * 128;
     static constexpr int kSmem = 1024 + kStages * (kA + kB) + kCodeStages * kCodes;
     static constexpr int kRedStride = 132;                           // floats of a row of x in the cluster's sum
     static_assert(NTOK * kRedStride * 4 <= kSmem - 1024, "the totals fit into the operands' memory");
 };
-constexpr int kTcThreads = 512;
 constexpr int kTcRows = 128;
-
-enum : int { kTcDense = 0, kTcExperts = 1 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* map, int x, int y, int z, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
             smem_u32(dst_smem)),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-// Four rows of a 2-D map whose box is one row high, to consecutive rows in shared memory.
-__device__ __forceinline__ void tma_gather4(void* dst_smem, const void* map, int x, int4 rows, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
-            smem_u32(dst_smem)),
-        "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(smem_u32(bar))
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -103,7 +93,7 @@ __device__ __forceinline__ uint4 convert8(uint32_t c, uint32_t flip, uint32_t z2
 }
 
 template <int G, int NTOK, bool Z>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     base_tc_kernel(BaseArgs a, const __grid_constant__ CUtensorMap codes_map,
                    const __grid_constant__ CUtensorMap x_map, bool scale_f32, bool y_f32, int n_split) {
     using C = TcConfig<NTOK>;
@@ -111,7 +101,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages], s_cfull[C::kCodeStages], s_cempty[C::kCodeStages],
         s_afull[2], s_aempty[2], s_done;
     __shared__ uint32_t s_tmem;
-    __shared__ __align__(16) int s_xrow[NTOK];                       // rows of x; one past the last where there is none
+    __shared__ int s_xrow[NTOK];         // -1: the row of y is not written
     __shared__ int s_unit[3];
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
@@ -136,10 +126,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (lane >= o) upto += v;
                 }
                 const int k = (int)blockIdx.y - (before + upto - units);
-                if (k >= 0 && k < units) {
+                if (k >= 0 && k < units) {       // an expert's rows in units of even size
                     s_unit[0] = e;
-                    s_unit[1] = first + k * NTOK;
-                    s_unit[2] = min(end, first + (k + 1) * NTOK);
+                    s_unit[1] = first + (int)((int64_t)(end - first) * k / units);
+                    s_unit[2] = first + (int)((int64_t)(end - first) * (k + 1) / units);
                 }
                 found = __any_sync(0xffffffffu, k >= 0 && k < units);
                 before += __shfl_sync(0xffffffffu, upto, 31);
@@ -159,17 +149,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // this CTA's code stages of K (256 values) and operand stages (64)
     const int all = (a.d_in + 255) / 256;
     const int c0 = (int)((int64_t)all * rank / n_split), c1 = (int)((int64_t)all * (rank + 1) / n_split);
-    const int k_begin = c0 * 256, k_end = min(a.d_in, c1 * 256), n_k = (k_end - k_begin + 63) / 64;
+    const int k_begin = c0 * 256, k_end = min(a.d_in, c1 * 256), n_k = (k_end - k_begin + C::kStageK - 1) / C::kStageK;
+    const int n_pad = (n_tok + 15) / 16 * 16;    // columns of the MMAs
     const int groups = a.d_in / G;
 
     if (tid < NTOK) {
-        int r = a.x_rows;
+        int r = -1;
         if (tid < n_tok) {
             r = row0 + tid;
             if (a.slot_of) {
                 const int slot = a.slot_of[r];
-                r = slot >= 0 && slot / a.k < a.x_rows ? slot / a.k : a.x_rows;
-                if (r == a.x_rows) atomicOr(&g_err_base_tc, kErrRows);
+                if (slot < 0 || slot / a.k >= a.x_rows) r = -1;       // reported by the gather
             }
         }
         s_xrow[tid] = r;
@@ -209,7 +199,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     int n_x = 0;                         // stages of x asked for
     if (warp < 4) {
-        if constexpr (NTOK == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 0) {
             if (lane == 0) {
                 int i = 0;
@@ -224,7 +214,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_wait(&s_cfull[j % C::kCodeStages], (j / C::kCodeStages) & 1, &g_err_base_tc);
             }
         } else if (warp == 1) {
-            const uint32_t idesc = idesc_bf16_f32(128, NTOK, false, false);
+            const uint32_t idesc = idesc_bf16_f32(128, n_pad, false, false);
             const uint64_t adesc = smem_desc_sw128(smem_u32(stages), 16, 1024), bdesc = smem_desc_sw128(smem_u32(stages) + C::kA, 16, 1024);
             int gi = 0;                  // groups begun
             int s = 0, buf = 0;
@@ -232,12 +222,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 wait(&s_full[s], (kt / C::kStages) & 1);
                 tc_fence_after();
                 const uint64_t at = (uint64_t)(s * ((C::kA + C::kB) / 16));
-                const int steps = min(4, (k_end - k_begin - kt * 64) / 16);
+                const int steps = min(C::kStageK, k_end - k_begin - kt * C::kStageK) / 16;
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
+                for (int ks = 0; ks < C::kStageK / 16; ++ks) {
                     if (ks >= steps) break;
-                    const bool first = G == 128 ? ks == 0 && kt % 2 == 0 : G == 64 ? ks == 0 : ks % 2 == 0;
-                    const bool last = G == 128 ? ks == 3 && kt % 2 == 1 : G == 64 ? ks == 3 : ks % 2 == 1;
+                    constexpr int kPer = G / 16;                     // steps of a group, which may take two stages
+                    const bool first = G > C::kStageK ? ks == 0 && kt % 2 == 0 : ks % kPer == 0;
+                    const bool last = G > C::kStageK ? ks == C::kStageK / 16 - 1 && kt % 2 == 1 : ks % kPer == kPer - 1;
                     if (first) {
                         if (gi >= 2) {
                             wait(&s_aempty[gi % 2], (gi / 2 - 1) & 1);
@@ -245,7 +236,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         buf = gi++ % 2;
                     }
-                    mma_elected(tmem + buf * NTOK, adesc + at + ks * 2, bdesc + at + ks * 2, idesc, !first);
+                    mma_elected(tmem + buf * NTOK, adesc + at + (ks / 4) * (128 * 128 / 16) + ks % 4 * 2,
+                                bdesc + at + (ks / 4) * (NTOK * 128 / 16) + ks % 4 * 2, idesc, !first);
                     if (last) commit_elected(&s_afull[buf]);
                 }
                 commit_elected(&s_empty[s]);
@@ -254,20 +246,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             commit_elected(&s_done);     // no MMA is left in flight
             mbar_wait(&s_done, 0, &g_err_base_tc);
         } else {
-            // x: consecutive rows by one tiled load a stage, else four rows a load; rows that do not exist read as 0
-            for (int kt = 0; warp == 2 && kt < n_k; ++kt) {
+            for (int kt = 0; warp == 2 && lane == 0 && kt < n_k; ++kt) {
                 const int s = kt % C::kStages;
                 if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
                 if (*abort_flag) break;
                 uint8_t* bs = stages + s * (C::kA + C::kB) + C::kA;
-                if (lane == 0) mbar_arrive_expect_tx(&s_full[s], C::kB);
-                __syncwarp();
-                if (!a.slot_of) {
-                    if (lane == 0) tma_load_2d(bs, &x_map, k_begin + kt * 64, row0, &s_full[s]);
-                } else {
+                mbar_arrive_expect_tx(&s_full[s], C::kB);
 #pragma unroll
-                    for (int r = lane * 4; r < NTOK; r += 128) tma_gather4(bs + r * 128, &x_map, k_begin + kt * 64, *reinterpret_cast<const int4*>(&s_xrow[r]), &s_full[s]);
-                }
+                for (int i = 0; i < C::kStageK / 64; ++i) tma_load_2d(bs + i * NTOK * 128, &x_map, k_begin + kt * C::kStageK + i * 64, row0, &s_full[s]);
                 n_x = kt + 1;
             }
             if (*abort_flag)             // no copy is left in flight
@@ -275,43 +261,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         __syncwarp();
     } else if (warp < 4 + C::kConvert) {
-        if constexpr (NTOK == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; with two parts they take alternate stages
-        constexpr int kParts = C::kConvert / 4;
-        constexpr int kZ = G >= 64 ? 1 : 2;                          // groups of a stage
+        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; the two halves of the warps take alternate stages
+        constexpr int kHalves = C::kStageK / 64;                     // 64 values: 128 bytes of A
+        constexpr int kZ = G >= 64 ? 1 : 2;                          // groups of 64 values, at least one
         const uint8_t* zrow = Z ? a.zeros + ((int64_t)e * a.d_out + min(n0 + r, a.d_out - 1)) * groups : nullptr;
-        uint32_t z_next[kZ] = {};
+        uint32_t z_next[kHalves][kZ] = {};
         const auto load_zeros = [&](int kt) {
             if constexpr (Z)
 #pragma unroll
-                for (int i = 0; i < kZ; ++i) z_next[i] = zrow[min((k_begin + kt * 64 + 32 * i) / G, groups - 1)];
+                for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                    for (int i = 0; i < kZ; ++i) z_next[h][i] = zrow[min((k_begin + kt * C::kStageK + 64 * h + 32 * i) / G, groups - 1)];
         };
         load_zeros(part);
         const uint32_t at = (r >> 3) * 1024 + (r & 7) * 128;
-        for (int kt = part; kt < n_k; kt += kParts) {
-            uint32_t z2[kZ];
+        constexpr int kPerCodes = 256 / C::kStageK;
+        for (int kt = part; kt < n_k; kt += 2) {
+            uint32_t z2[kHalves][kZ];
 #pragma unroll
-            for (int i = 0; i < kZ; ++i) z2[i] = Z ? (0x4300u | z_next[i]) * 0x10001u : 0x43084308u;
-            load_zeros(kt + kParts);
-            const int s = kt % C::kStages, cs = kt / 4 % C::kCodeStages;
-            wait(&s_cfull[cs], (kt / 4 / C::kCodeStages) & 1);
-            if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                for (int i = 0; i < kZ; ++i) z2[h][i] = Z ? (0x4300u | z_next[h][i]) * 0x10001u : 0x43084308u;
+            load_zeros(kt + 2);
+            const int s = kt % C::kStages, ci = kt / kPerCodes, cs = ci % C::kCodeStages;
+            wait(&s_cfull[cs], (ci / C::kCodeStages) & 1);
             const uint8_t* cp = codes + cs * C::kCodes + at;
+            uint4 v[2 * kHalves];
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) v[i] = *reinterpret_cast<const uint4*>(cp + ((kt % kPerCodes * 2 * kHalves + i) ^ (r & 7)) * 16);
+            if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
             uint8_t* ap = stages + s * (C::kA + C::kB) + at;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 v = *reinterpret_cast<const uint4*>(cp + ((kt % 4 * 2 + h) ^ (r & 7)) * 16);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4*>(ap + ((4 * h + i) ^ (r & 7)) * 16) = convert8(w[i], Z ? 0u : 0x08080808u, z2[kZ == 1 ? 0 : h]);
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4*>(ap + i / 2 * (128 * 128) + ((i % 2 * 4 + j) ^ (r & 7)) * 16) =
+                        convert8(w[j], Z ? 0u : 0x08080808u, z2[i / 2][kZ == 1 ? 0 : i % 2]);
             }
             fence_proxy_async_smem();
             mbar_arrive(&s_full[s]);
-            if (kt % 4 / kParts == 4 / kParts - 1) mbar_arrive(&s_cempty[cs]);
+            if (kt % kPerCodes / 2 == kPerCodes / 2 - 1) mbar_arrive(&s_cempty[cs]);
         }
     } else {
-        if constexpr (NTOK == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (NTOK > 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");   // 5 warpgroups of 96 at launch: 3 x 48 + 2 x 168
         const int erow = (warp % 4) * 32 + lane, ecol = (warp - 4 - C::kConvert) / 4 * C::kCols;
         float total[C::kCols];
         const int64_t srow = ((int64_t)e * a.d_out + min(n0 + erow, a.d_out - 1)) * groups + k_begin / G;
@@ -330,21 +324,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             wait(&s_afull[buf], (g / 2) & 1);
             tc_fence_after();
             const uint32_t from = tmem + buf * NTOK + ecol + ((uint32_t)(warp % 4 * 32) << 16);
-            if constexpr (C::kCols % 32 == 0) {
 #pragma unroll
-                for (int c = 0; c < C::kCols; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(from + c, v);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) total[c + i] = fmaf(sc, __uint_as_float(v[i]), total[c + i]);
-                }
-            } else {
+            for (int c = 0; c < C::kCols; c += 16) {
+                if (ecol + c >= n_pad) break;
                 uint32_t v[16];
-                tmem_ld_x16(from, v);
+                tmem_ld_x16(from + c, v);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) total[i] = fmaf(sc, __uint_as_float(v[i]), total[i]);
+                for (int i = 0; i < 16; ++i) total[c + i] = fmaf(sc, __uint_as_float(v[i]), total[c + i]);
             }
             tc_fence_before();
             __syncwarp();
@@ -356,7 +343,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         } else if (!*abort_flag && n0 + erow < a.d_out) {
 #pragma unroll
             for (int i = 0; i < C::kCols; ++i)
-                if (ecol + i < n_tok && s_xrow[ecol + i] < a.x_rows) {
+                if (ecol + i < n_tok && s_xrow[ecol + i] >= 0) {
                     const int64_t to = (int64_t)(row0 + ecol + i) * a.ldy + n0 + erow;
                     if (y_f32) static_cast<float*>(a.y)[to] = total[i];
                     else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(total[i]));
@@ -367,14 +354,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (n_split > 1) {                   // the CTAs' totals, in a fixed order
         cluster_sync();
         const uint32_t base = smem_u32(red);
-        for (int i = rank * kTcThreads + tid; i < n_tok * 128; i += n_split * kTcThreads) {
+        for (int i = rank * C::kThreads + tid; i < n_tok * 128; i += n_split * C::kThreads) {
             const int t = i / 128, n = i % 128;
             float v[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) v[c] = c < n_split ? ld_cluster_f32(map_cluster(base + (t * C::kRedStride + n) * 4, c)) : 0.0f;
 #pragma unroll
             for (int c = 1; c < 8; ++c) v[0] += v[c];
-            if (n0 + n < a.d_out && s_xrow[t] < a.x_rows && !*abort_flag) {
+            if (n0 + n < a.d_out && s_xrow[t] >= 0 && !*abort_flag) {
                 const int64_t to = (int64_t)(row0 + t) * a.ldy + n0 + n;
                 if (y_f32) static_cast<float*>(a.y)[to] = v[0];
                 else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
@@ -413,9 +400,9 @@ cudaError_t encode_codes(CUtensorMap* map, const BaseArgs& a) {
     const cuuint32_t box[3] = {128, kTcRows, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.codes, dims, strides, box);
 }
-// x in boxes of 64 values of `rows` rows (1 for loads of four rows of any place).
+// x in boxes of 64 values of `rows` rows; with slots, it has been gathered into a row for each row of y.
 cudaError_t encode_x(CUtensorMap* map, const BaseArgs& a, int rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)a.d_in, (cuuint64_t)a.x_rows}, strides[1] = {(cuuint64_t)a.ldx * 2};
+    const cuuint64_t dims[2] = {(cuuint64_t)a.d_in, (cuuint64_t)(a.slot_of ? a.rows : a.x_rows)}, strides[1] = {(cuuint64_t)a.ldx * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)rows};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, dims, strides, box);
 }
@@ -427,15 +414,20 @@ cudaError_t launch_t(const BaseArgs& a, bool scale_f32, bool y_f32, cudaStream_t
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (err != cudaSuccess) return err;
     CUtensorMap map, x_map;
-    if ((err = encode_codes(&map, a)) != cudaSuccess || (err = encode_x(&x_map, a, a.slot_of ? 1 : NTOK)) != cudaSuccess) return err;
+    if ((err = encode_codes(&map, a)) != cudaSuccess || (err = encode_x(&x_map, a, NTOK)) != cudaSuccess) return err;
     const int tiles = (a.d_out + kTcRows - 1) / kTcRows, k_stages = (a.d_in + 255) / 256;
     const int64_t units = a.offsets ? (int64_t)a.rows / NTOK + std::min(a.rows, a.experts) : ((int64_t)a.rows + NTOK - 1) / NTOK;
+    // the split of K that takes the fewest rounds of 148 CTAs, each counted with four code stages' worth of fixed cost
     int split = 1;
-    if (!a.offsets)
-        while (split < 8 && 4 * split <= k_stages && tiles * units * split < 148) split *= 2;
+    double best = 0;
+    for (int c = 1; c <= std::min(8, k_stages); ++c) {
+        const double cost = (double)((tiles * units * c + 147) / 148) * ((k_stages + c - 1) / c + 4);
+        if (c == 1 || cost < 0.97 * best) best = cost, split = c;
+        if (a.offsets) break;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)units);
-    cfg.blockDim = dim3(kTcThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -33,7 +33,17 @@ def experts(**kw):
     a = dict(x_rows=4, E=3, offsets=P, slot_of=None, k=1, rows=4)
     a.update(kw)
     return sg.load_library().sgmv_base_product_experts(P, 64, a["x_rows"], 64, 8, a["E"], P, P, 0, None, 64, a["offsets"], a["slot_of"],
-                                                       a["k"], a["rows"], P, 8, 0, None)
+                                                       a["k"], a["rows"], P, 8, 0, a.get("ws"), a.get("nws", 0), None)
+
+
+def test_base_product_experts_workspace():
+    lib = sg.load_library()
+    assert lib.sgmv_base_product_experts_workspace(16, 64, 1) == 0 and lib.sgmv_base_product_experts_workspace(0, 64, 3) == 0
+    assert lib.sgmv_base_product_experts_workspace(17, 64, 1) == 17 * 128
+    assert lib.sgmv_base_product_experts_workspace(-1, 64, 1) == lib.sgmv_base_product_experts_workspace(1, 64, 4097) == -1
+    many = dict(rows=400, x_rows=400, slot_of=P)
+    assert experts(**many) == 1 and b"workspace" in lib.sgmv_last_error()
+    assert experts(**many, ws=P + 8, nws=1 << 20) == 1 and experts(**many, ws=P, nws=400 * 128 - 1) == 8
 
 
 @pytest.mark.parametrize("kw", [dict(E=0), dict(E=4097), dict(offsets=None), dict(offsets=P + 2), dict(x_rows=3), dict(slot_of=P, k=0),
