@@ -57,23 +57,49 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
-// tc_mma_bf16 and tc_commit by one lane of a converged warp.  The election is inside, so that the operands stay in
-// uniform registers; under a branch on the lane each MMA took about 200 cycles to issue.
-__device__ __forceinline__ void mma_elected(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
-        : "memory");
+// One lane of a converged warp.  MMAs under this election have their operands in uniform registers; under a branch on
+// the lane number each took about 200 cycles to issue, elected one by one about 100.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
-__device__ __forceinline__ void commit_elected(uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-        : "memory");
+
+// The scales or zero points of N consecutive groups of a row, as loaded; `left`: groups of the row from the first on,
+// `vec`: at least N, aligned to their size.
+template <int N>
+__device__ __forceinline__ void load_scales(uint32_t (&w)[N], const void* scales, int64_t at, int left, bool f32, bool vec) {
+    if (vec) {
+        if constexpr (N == 2) {
+            if (f32) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(static_cast<const uint32_t*>(scales) + at);
+            else w[0] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(scales) + at);
+        } else {
+            if (f32) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(scales) + at);
+            else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(scales) + at);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < left) {
+            if (f32) w[i] = static_cast<const uint32_t*>(scales)[at + i];
+            else w[i / 2] |= (uint32_t)static_cast<const uint16_t*>(scales)[at + i] << (i % 2 * 16);
+        }
+}
+template <int N>
+__device__ __forceinline__ float scale_of(const uint32_t (&w)[N], int i, bool f32) {
+    return f32 ? __uint_as_float(w[i]) : i % 2 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+}
+template <int N>
+__device__ __forceinline__ uint32_t load_zeros(const uint8_t* zeros, int64_t at, int left, bool vec) {
+    if (vec) return N == 2 ? *reinterpret_cast<const uint16_t*>(zeros + at) : *reinterpret_cast<const uint32_t*>(zeros + at);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < left) w |= (uint32_t)zeros[at + i] << (8 * i);
+    return w;
 }
 
 // Eight codes (value i in bits 4i..4i+3) less the zero point, as eight bf16 in order.  bf16 128 + n has the bits
@@ -95,8 +121,9 @@ __device__ __forceinline__ uint4 convert8(uint32_t c, uint32_t flip, uint32_t z2
 template <int G, int NTOK, bool Z>
 __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     base_tc_kernel(BaseArgs a, const __grid_constant__ CUtensorMap codes_map,
-                   const __grid_constant__ CUtensorMap x_map, bool scale_f32, bool y_f32, int n_split) {
+                   const __grid_constant__ CUtensorMap x_map, bool scale_f32, bool y_f32, bool vec, int n_split) {
     using C = TcConfig<NTOK>;
+    constexpr int kSpan = G == 32 ? 128 : 256, kGroups = kSpan / G;  // K values whose scales are loaded together
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages], s_cfull[C::kCodeStages], s_cempty[C::kCodeStages],
         s_afull[2], s_aempty[2], s_done;
@@ -199,7 +226,7 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
 
     int n_x = 0;                         // stages of x asked for
     if (warp < 4) {
-        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
             if (lane == 0) {
                 int i = 0;
@@ -223,12 +250,11 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
                 tc_fence_after();
                 const uint64_t at = (uint64_t)(s * ((C::kA + C::kB) / 16));
                 const int steps = min(C::kStageK, k_end - k_begin - kt * C::kStageK) / 16;
+                constexpr int kPer = G / 16, kSeg = (G < C::kStageK ? G : C::kStageK) / 16;      // steps of a group; of it in a stage
 #pragma unroll
-                for (int ks = 0; ks < C::kStageK / 16; ++ks) {
-                    if (ks >= steps) break;
-                    constexpr int kPer = G / 16;                     // steps of a group, which may take two stages
-                    const bool first = G > C::kStageK ? ks == 0 && kt % 2 == 0 : ks % kPer == 0;
-                    const bool last = G > C::kStageK ? ks == C::kStageK / 16 - 1 && kt % 2 == 1 : ks % kPer == kPer - 1;
+                for (int k0 = 0; k0 < C::kStageK / 16; k0 += kSeg) {
+                    if (k0 >= steps) break;
+                    const bool first = kPer == kSeg || kt % 2 == 0, last = kPer == kSeg || kt % 2 == 1;
                     if (first) {
                         if (gi >= 2) {
                             wait(&s_aempty[gi % 2], (gi / 2 - 1) & 1);
@@ -236,14 +262,21 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
                         }
                         buf = gi++ % 2;
                     }
-                    mma_elected(tmem + buf * NTOK, adesc + at + (ks / 4) * (128 * 128 / 16) + ks % 4 * 2,
-                                bdesc + at + (ks / 4) * (NTOK * 128 / 16) + ks % 4 * 2, idesc, !first);
-                    if (last) commit_elected(&s_afull[buf]);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < kSeg; ++i) {
+                            const int ks = k0 + i;
+                            tc_mma_bf16(tmem + buf * NTOK, adesc + at + (ks / 4) * (128 * 128 / 16) + ks % 4 * 2,
+                                        bdesc + at + (ks / 4) * (NTOK * 128 / 16) + ks % 4 * 2, idesc, i > 0 || !first);
+                        }
+                        if (last) tc_commit(&s_afull[buf]);
+                        if (k0 + kSeg >= steps) tc_commit(&s_empty[s]);
+                    }
+                    __syncwarp();
                 }
-                commit_elected(&s_empty[s]);
                 s = s == C::kStages - 1 ? 0 : s + 1;
             }
-            commit_elected(&s_done);     // no MMA is left in flight
+            if (elect_one()) tc_commit(&s_done);     // no MMA is left in flight
             mbar_wait(&s_done, 0, &g_err_base_tc);
         } else {
             for (int kt = 0; warp == 2 && lane == 0 && kt < n_k; ++kt) {
@@ -261,29 +294,25 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp < 4 + C::kConvert) {
-        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; the two halves of the warps take alternate stages
         constexpr int kHalves = C::kStageK / 64;                     // 64 values: 128 bytes of A
-        constexpr int kZ = G >= 64 ? 1 : 2;                          // groups of 64 values, at least one
-        const uint8_t* zrow = Z ? a.zeros + ((int64_t)e * a.d_out + min(n0 + r, a.d_out - 1)) * groups : nullptr;
-        uint32_t z_next[kHalves][kZ] = {};
-        const auto load_zeros = [&](int kt) {
-            if constexpr (Z)
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                    for (int i = 0; i < kZ; ++i) z_next[h][i] = zrow[min((k_begin + kt * C::kStageK + 64 * h + 32 * i) / G, groups - 1)];
+        const int64_t zrow = ((int64_t)e * a.d_out + min(n0 + r, a.d_out - 1)) * groups;
+        const auto zeros_at = [&](int k) {
+            const int g = min(k, a.d_in - 1) / kSpan * kGroups;
+            return load_zeros<kGroups>(a.zeros, zrow + g, groups - g, vec);
         };
-        load_zeros(part);
+        uint32_t z_now = 0, z_next = Z ? zeros_at(k_begin + part * C::kStageK) : 0;
+        int z_span = -1;                 // the span that z_now is of
         const uint32_t at = (r >> 3) * 1024 + (r & 7) * 128;
         constexpr int kPerCodes = 256 / C::kStageK;
         for (int kt = part; kt < n_k; kt += 2) {
-            uint32_t z2[kHalves][kZ];
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                for (int i = 0; i < kZ; ++i) z2[h][i] = Z ? (0x4300u | z_next[h][i]) * 0x10001u : 0x43084308u;
-            load_zeros(kt + 2);
+            const int k = k_begin + kt * C::kStageK;
+            if (Z && k / kSpan != z_span) {
+                z_span = k / kSpan;
+                z_now = z_next;
+                z_next = zeros_at(k + (kSpan > 2 * C::kStageK ? kSpan : 2 * C::kStageK));    // of this warp's next span
+            }
             const int s = kt % C::kStages, ci = kt / kPerCodes, cs = ci % C::kCodeStages;
             wait(&s_cfull[cs], (ci / C::kCodeStages) & 1);
             const uint8_t* cp = codes + cs * C::kCodes + at;
@@ -295,47 +324,57 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2 * kHalves; ++i) {
                 const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                const uint32_t z2 = Z ? (0x4300u | (z_now >> ((k + 32 * i) % kSpan / G * 8) & 0xffu)) * 0x10001u : 0x43084308u;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     *reinterpret_cast<uint4*>(ap + i / 2 * (128 * 128) + ((i % 2 * 4 + j) ^ (r & 7)) * 16) =
-                        convert8(w[j], Z ? 0u : 0x08080808u, z2[i / 2][kZ == 1 ? 0 : i % 2]);
+                        convert8(w[j], Z ? 0u : 0x08080808u, z2);
             }
             fence_proxy_async_smem();
             mbar_arrive(&s_full[s]);
             if (kt % kPerCodes / 2 == kPerCodes / 2 - 1) mbar_arrive(&s_cempty[cs]);
         }
     } else {
-        if constexpr (NTOK > 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");   // 5 warpgroups of 96 at launch: 3 x 48 + 2 x 168
+        if constexpr (NTOK > 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");   // 5 warpgroups of 96 at launch: 3 x 40 + 2 x 176
         const int erow = (warp % 4) * 32 + lane, ecol = (warp - 4 - C::kConvert) / 4 * C::kCols;
         float total[C::kCols];
-        const int64_t srow = ((int64_t)e * a.d_out + min(n0 + erow, a.d_out - 1)) * groups + k_begin / G;
-        const auto scale = [&](int g) {
-            return scale_f32 ? static_cast<const float*>(a.scales)[srow + g]
-                             : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.scales)[srow + g] << 16);
-        };
+        const int64_t srow = ((int64_t)e * a.d_out + min(n0 + erow, a.d_out - 1)) * groups;
 #pragma unroll
         for (int i = 0; i < C::kCols; ++i) total[i] = 0.0f;
-        const int n_g = (k_end - k_begin) / G;
-        float next = scale(0);
-        for (int g = 0; g < n_g; ++g) {
-            const float sc = next;
-            if (g + 1 < n_g) next = scale(g + 1);
-            const int buf = g % 2;
-            wait(&s_afull[buf], (g / 2) & 1);
-            tc_fence_after();
-            const uint32_t from = tmem + buf * NTOK + ecol + ((uint32_t)(warp % 4 * 32) << 16);
+        const int g0 = k_begin / G, g1 = k_end / G;
+        const auto add = [&](uint32_t (&v)[16], int c, float sc) {
 #pragma unroll
-            for (int c = 0; c < C::kCols; c += 16) {
-                if (ecol + c >= n_pad) break;
-                uint32_t v[16];
-                tmem_ld_x16(from + c, v);
-                tmem_ld_wait();
+            for (int i = 0; i < 16; ++i) total[c + i] = fmaf(sc, __uint_as_float(v[i]), total[c + i]);
+        };
+        uint32_t now[kGroups], next[kGroups];
+        load_scales(next, a.scales, srow + g0, groups - g0, scale_f32, vec);
+        for (int gs = g0; gs < g1; gs += kGroups) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) total[c + i] = fmaf(sc, __uint_as_float(v[i]), total[c + i]);
+            for (int i = 0; i < kGroups; ++i) now[i] = next[i];
+            if (gs + kGroups < g1) load_scales(next, a.scales, srow + gs + kGroups, groups - gs - kGroups, scale_f32, vec);
+#pragma unroll
+            for (int gi = 0; gi < kGroups; ++gi) {
+                if (gs + gi >= g1) break;
+                const float sc = scale_of(now, gi, scale_f32);
+                const int buf = gi % 2;  // a span has an even number of groups
+                wait(&s_afull[buf], ((gs - g0 + gi) / 2) & 1);
+                tc_fence_after();
+                const uint32_t from = tmem + buf * NTOK + ecol + ((uint32_t)(warp % 4 * 32) << 16);
+                uint32_t v0[16], v1[16];     // a load runs while the other's values are added
+                if (ecol < n_pad) tmem_ld_x16(from, v0);
+#pragma unroll
+                for (int c = 0; c < C::kCols; c += 32) {
+                    tmem_ld_wait();
+                    if (ecol + c + 16 < n_pad) tmem_ld_x16(from + c + 16, v1);
+                    if (ecol + c < n_pad) add(v0, c, sc);
+                    tmem_ld_wait();
+                    if (c + 32 < C::kCols && ecol + c + 32 < n_pad) tmem_ld_x16(from + c + 32, v0);
+                    if (ecol + c + 16 < n_pad) add(v1, c + 16, sc);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_aempty[buf]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_aempty[buf]);
         }
         if (n_split > 1) {               // the last group's MMAs are complete, and so are all before them
 #pragma unroll
@@ -425,6 +464,9 @@ cudaError_t launch_t(const BaseArgs& a, bool scale_f32, bool y_f32, cudaStream_t
         if (c == 1 || cost < 0.97 * best) best = cost, split = c;
         if (a.offsets) break;
     }
+    constexpr int kSpan = G == 32 ? 128 : 256;
+    const auto at = [](const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+    const bool vec = a.d_in % kSpan == 0 && at(a.scales, 16) && at(a.zeros, 4);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)units);
     cfg.blockDim = dim3(C::kThreads);
@@ -437,7 +479,7 @@ cudaError_t launch_t(const BaseArgs& a, bool scale_f32, bool y_f32, cudaStream_t
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, a, map, x_map, scale_f32, y_f32, split);
+    return cudaLaunchKernelEx(&cfg, kern, a, map, x_map, scale_f32, y_f32, vec, split);
 }
 
 template <int G, bool Z>
