@@ -17,30 +17,34 @@ namespace {
 // y^T = W x^T in tiles of 128 rows of W and NTOK rows of x.  tcgen05.mma takes the codes less their zero points,
 // exact in bf16, as its A operand and x as B, and sums one group of K values at a time into tensor memory; the
 // epilogue warps fetch each group's sums and add them, times the row's fp32 scale, to totals in registers, so that
-// no scale is ever rounded to bf16.  Two accumulators alternate between the groups.
+// no scale is ever rounded to bf16.  The converted codes go straight to tensor memory (a thread holds a row, which is
+// a lane there): through shared memory they made its bandwidth the bound, at 61 % of the MMA rate.  There is room
+// for two accumulators of 128 columns beside them, so 256 rows of x take two passes over each group's K values.
 //
-// What bounds it: with 256 rows of x, the tensor cores (a group of 128 is 1024 cycles of MMA against about 600
-// issue slots of conversion and epilogue per scheduler); with few, the conversion of the codes, as in the kernel
-// for few rows, and the stream of codes.
+// What bounds it: with 256 rows of x, shared memory (x written and read once, 1152 cycles for 128 K values) and the
+// tensor cores (1024); with groups of 32, the epilogue; with few rows, the conversion and the stream of codes.
 //
-// Roles: warp 0 streams codes (TMA, stages of 128 rows x 256 values), 1 issues the MMAs, 2 copies x (TMA), 8 warps
-// turn codes into the A operand (a thread a row, half of the warps each stage), the rest are the epilogue.  K is
-// split over the CTAs of a cluster when there are few tiles; their totals meet in shared memory in a fixed order.
+// Roles: warp 0 streams codes (TMA, stages of 128 rows x 256 values), 1 issues the MMAs, 2 copies x (TMA), 4 or 8
+// warps convert (of 8, half take each stage), the rest are the epilogue, many where a pass leaves them little time.  K is split over the CTAs of a cluster when there are
+// few tiles; their totals meet in shared memory in a fixed order.
 template <int NTOK>
 struct TcConfig {
-    static constexpr int kConvert = 8;                               // warps
-    static constexpr int kEpilogue = NTOK <= 64 ? 4 : 8;
+    static constexpr int kConvert = NTOK == 256 ? 4 : 8;             // warps
+    static constexpr int kEpilogue = NTOK <= 64 ? 4 : NTOK == 128 ? 8 : 16;
     static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
-    static constexpr int kCols = NTOK / (kEpilogue / 4);             // columns of an epilogue warp
-    static constexpr int kStageK = NTOK <= 64 ? 128 : 64;            // K values of an operand stage
-    static constexpr int kStages = NTOK == 128 ? 4 : 3;
-    static constexpr int kCodeStages = 3;                            // of 256 K values
-    static constexpr int kA = 128 * 2 * kStageK, kB = NTOK * 2 * kStageK, kCodes = 128 * 128;
-    static constexpr int kSmem = 1024 + kStages * (kA + kB) + kCodeStages * kCodes;
+    static constexpr int kPassCols = NTOK < 128 ? NTOK : 128;        // columns of an accumulator
+    static constexpr int kPasses = NTOK / kPassCols;
+    static constexpr int kCols = kPassCols / (kEpilogue / 4);        // of them, an epilogue warp's
+    static constexpr int kStages = NTOK <= 64 ? 4 : 3;               // of 128 K values
+    static constexpr int kCodeStages = NTOK == 256 ? 2 : 3;          // of 256 K values
+    static constexpr int kB = NTOK * 256, kCodes = 128 * 128;
+    static constexpr int kSmem = 1024 + kStages * kB + kCodeStages * kCodes;
+    static constexpr int kTmemA = 2 * kPassCols, kTmem = kTmemA + kStages * 64 <= 256 ? 256 : 512;    // columns
     static constexpr int kRedStride = 132;                           // floats of a row of x in the cluster's sum
     static_assert(NTOK * kRedStride * 4 <= kSmem - 1024, "the totals fit into the operands' memory");
+    static_assert(kSmem <= 227 * 1024 && kTmemA + kStages * 64 <= 512, "the stages fit");
 };
-constexpr int kTcRows = 128;
+constexpr int kTcRows = 128, kStageK = 128;
 
 __device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* map, int x, int y, int z, uint64_t* bar) {
     asm volatile(
@@ -55,6 +59,24 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] * B[smem]^T: A has a lane a row and two consecutive K values a column.
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
 }
 
 // One lane of a converged warp.  MMAs under this election have their operands in uniform registers; under a branch on
@@ -105,7 +127,7 @@ __device__ __forceinline__ uint32_t load_zeros(const uint8_t* zeros, int64_t at,
 // Eight codes (value i in bits 4i..4i+3) less the zero point, as eight bf16 in order.  bf16 128 + n has the bits
 // 0x4300 | n for n < 128, so inserting the code and subtracting 128 + z is exact.  `flip` is 0x08080808 for two's
 // complement codes (n ^ 8 is the value plus 8; then z is 8).
-__device__ __forceinline__ uint4 convert8(uint32_t c, uint32_t flip, uint32_t z2) {
+__device__ __forceinline__ void convert8(uint32_t c, uint32_t flip, uint32_t z2, uint32_t* out) {
     const uint32_t even = (c & 0x0f0f0f0fu) ^ flip, odd = ((c >> 4) & 0x0f0f0f0fu) ^ flip;
     const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
     uint32_t p[4] = {__byte_perm(lo, 0x43u, 0x4140), __byte_perm(lo, 0x43u, 0x4342), __byte_perm(hi, 0x43u, 0x4140),
@@ -113,9 +135,8 @@ __device__ __forceinline__ uint4 convert8(uint32_t c, uint32_t flip, uint32_t z2
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&p[i]), *reinterpret_cast<const __nv_bfloat162*>(&z2));
-        p[i] = *reinterpret_cast<const uint32_t*>(&d);
+        out[i] = *reinterpret_cast<const uint32_t*>(&d);
     }
-    return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
 template <int G, int NTOK, bool Z>
@@ -133,8 +154,8 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
     const int rank = blockIdx.x % n_split, n0 = (int)(blockIdx.x / n_split) * kTcRows;
-    uint8_t* stages = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;  // [kStages][A, B]
-    uint8_t* codes = stages + C::kStages * (C::kA + C::kB);                  // [kCodeStages]
+    uint8_t* stages = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;  // [kStages][2][NTOK] rows of 64 values of x
+    uint8_t* codes = stages + C::kStages * C::kB;                            // [kCodeStages][128] rows of 256 codes
 
     // the unit: up to NTOK consecutive rows of y of one matrix
     if (a.offsets) {
@@ -173,11 +194,12 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     const int e = s_unit[0], row0 = s_unit[1], n_tok = s_unit[2] - row0;
     if (n_tok <= 0) return;              // the same for every CTA of the cluster
 
-    // this CTA's code stages of K (256 values) and operand stages (64)
+    // this CTA's code stages of K (256 values) and operand stages (128)
     const int all = (a.d_in + 255) / 256;
     const int c0 = (int)((int64_t)all * rank / n_split), c1 = (int)((int64_t)all * (rank + 1) / n_split);
-    const int k_begin = c0 * 256, k_end = min(a.d_in, c1 * 256), n_k = (k_end - k_begin + C::kStageK - 1) / C::kStageK;
+    const int k_begin = c0 * 256, k_end = min(a.d_in, c1 * 256), n_k = (k_end - k_begin + kStageK - 1) / kStageK;
     const int n_pad = (n_tok + 15) / 16 * 16;    // columns of the MMAs
+    const int n_pass = (n_pad + C::kPassCols - 1) / C::kPassCols;
     const int groups = a.d_in / G;
 
     if (tid < NTOK) {
@@ -209,7 +231,7 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(&s_tmem, 2 * NTOK);
+        tmem_alloc(&s_tmem, C::kTmem);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -219,14 +241,22 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     // waits give up together: whoever runs out of time stops the others' waits too
     volatile int* abort_flag = &s_abort;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!*abort_flag && !mbar_wait(bar, parity, &g_err_base_tc)) *abort_flag = 1;
+        if (mbar_try_wait(bar, parity)) return;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, parity) && !*abort_flag)
+            if (clock64() - t0 > kWaitLimitCycles) {
+                atomicOr(&g_err_base_tc, kErrTimeout);
+                *abort_flag = 1;
+            }
     };
 
     float* red = reinterpret_cast<float*>(stages);                   // the CTA's totals, for its cluster
 
     int n_x = 0;                         // stages of x asked for
     if (warp < 4) {
-        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        // 5 warpgroups of 96 registers at launch: 48 + 2 x 56 + 2 x 160; or 6 of 80: 40 + 56 + 4 x 96
+        if constexpr (NTOK == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if constexpr (NTOK == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
             if (lane == 0) {
                 int i = 0;
@@ -241,38 +271,38 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
                     mbar_wait(&s_cfull[j % C::kCodeStages], (j / C::kCodeStages) & 1, &g_err_base_tc);
             }
         } else if (warp == 1) {
-            const uint32_t idesc = idesc_bf16_f32(128, n_pad, false, false);
-            const uint64_t adesc = smem_desc_sw128(smem_u32(stages), 16, 1024), bdesc = smem_desc_sw128(smem_u32(stages) + C::kA, 16, 1024);
-            int gi = 0;                  // groups begun
-            int s = 0, buf = 0;
+            const uint64_t bdesc = smem_desc_sw128(smem_u32(stages), 16, 1024);
+            int n = 0, s = 0;            // passes begun; the stage's slot
             for (int kt = 0; kt < n_k; ++kt) {
                 wait(&s_full[s], (kt / C::kStages) & 1);
                 tc_fence_after();
-                const uint64_t at = (uint64_t)(s * ((C::kA + C::kB) / 16));
-                const int steps = min(C::kStageK, k_end - k_begin - kt * C::kStageK) / 16;
-                constexpr int kPer = G / 16, kSeg = (G < C::kStageK ? G : C::kStageK) / 16;      // steps of a group; of it in a stage
+                const int n_groups = min(kStageK, k_end - k_begin - kt * kStageK) / G;
 #pragma unroll
-                for (int k0 = 0; k0 < C::kStageK / 16; k0 += kSeg) {
-                    if (k0 >= steps) break;
-                    const bool first = kPer == kSeg || kt % 2 == 0, last = kPer == kSeg || kt % 2 == 1;
-                    if (first) {
-                        if (gi >= 2) {
-                            wait(&s_aempty[gi % 2], (gi / 2 - 1) & 1);
+                for (int gi = 0; gi < kStageK / G; ++gi) {
+                    if (gi >= n_groups) break;
+#pragma unroll
+                    for (int p = 0; p < C::kPasses; ++p) {
+                        if (p >= n_pass) break;
+                        const int buf = n % 2;
+                        if (n >= 2) {
+                            wait(&s_aempty[buf], (n / 2 - 1) & 1);
                             tc_fence_after();
                         }
-                        buf = gi++ % 2;
-                    }
-                    if (elect_one()) {
+                        ++n;
+                        if (elect_one()) {
+                            const uint32_t idesc = idesc_bf16_f32(128, min(C::kPassCols, n_pad - p * C::kPassCols), false, false);
+                            const uint32_t d = tmem + buf * C::kPassCols, at = tmem + C::kTmemA + s * 64;
+                            const uint64_t bd = bdesc + (uint64_t)((s * C::kB + p * (C::kPassCols * 128)) / 16);
 #pragma unroll
-                        for (int i = 0; i < kSeg; ++i) {
-                            const int ks = k0 + i;
-                            tc_mma_bf16(tmem + buf * NTOK, adesc + at + (ks / 4) * (128 * 128 / 16) + ks % 4 * 2,
-                                        bdesc + at + (ks / 4) * (NTOK * 128 / 16) + ks % 4 * 2, idesc, i > 0 || !first);
+                            for (int i = 0; i < G / 16; ++i) {
+                                const int ks = gi * (G / 16) + i;
+                                tc_mma_bf16_ts(d, at + ks * 8, bd + (ks / 4) * (NTOK * 128 / 16) + ks % 4 * 2, idesc, i > 0);
+                            }
+                            tc_commit(&s_afull[buf]);
+                            if (gi == n_groups - 1 && p == n_pass - 1) tc_commit(&s_empty[s]);
                         }
-                        if (last) tc_commit(&s_afull[buf]);
-                        if (k0 + kSeg >= steps) tc_commit(&s_empty[s]);
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
                 s = s == C::kStages - 1 ? 0 : s + 1;
             }
@@ -283,10 +313,10 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
                 const int s = kt % C::kStages;
                 if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
                 if (*abort_flag) break;
-                uint8_t* bs = stages + s * (C::kA + C::kB) + C::kA;
+                uint8_t* bs = stages + s * C::kB;
                 mbar_arrive_expect_tx(&s_full[s], C::kB);
 #pragma unroll
-                for (int i = 0; i < C::kStageK / 64; ++i) tma_load_2d(bs + i * NTOK * 128, &x_map, k_begin + kt * C::kStageK + i * 64, row0, &s_full[s]);
+                for (int i = 0; i < 2; ++i) tma_load_2d(bs + i * NTOK * 128, &x_map, k_begin + kt * kStageK + i * 64, row0, &s_full[s]);
                 n_x = kt + 1;
             }
             if (*abort_flag)             // no copy is left in flight
@@ -294,96 +324,117 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp < 4 + C::kConvert) {
-        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; the two halves of the warps take alternate stages
-        constexpr int kHalves = C::kStageK / 64;                     // 64 values: 128 bytes of A
+        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; of two sets of warps each takes alternate stages
+        constexpr int kParts = C::kConvert / 4;
         const int64_t zrow = ((int64_t)e * a.d_out + min(n0 + r, a.d_out - 1)) * groups;
         const auto zeros_at = [&](int k) {
             const int g = min(k, a.d_in - 1) / kSpan * kGroups;
             return load_zeros<kGroups>(a.zeros, zrow + g, groups - g, vec);
         };
-        uint32_t z_now = 0, z_next = Z ? zeros_at(k_begin + part * C::kStageK) : 0;
+        uint32_t z_now = 0, z_next = Z ? zeros_at(k_begin + part * kStageK) : 0;
         int z_span = -1;                 // the span that z_now is of
-        const uint32_t at = (r >> 3) * 1024 + (r & 7) * 128;
-        constexpr int kPerCodes = 256 / C::kStageK;
-        for (int kt = part; kt < n_k; kt += 2) {
-            const int k = k_begin + kt * C::kStageK;
+        const uint32_t to = tmem + C::kTmemA + ((uint32_t)(warp % 4 * 32) << 16);
+        for (int kt = part; kt < n_k; kt += kParts) {
+            const int k = k_begin + kt * kStageK;
             if (Z && k / kSpan != z_span) {
                 z_span = k / kSpan;
                 z_now = z_next;
-                z_next = zeros_at(k + (kSpan > 2 * C::kStageK ? kSpan : 2 * C::kStageK));    // of this warp's next span
+                z_next = zeros_at(k + max(kSpan, kParts * kStageK));    // of this warp's next span
             }
-            const int s = kt % C::kStages, ci = kt / kPerCodes, cs = ci % C::kCodeStages;
+            const int s = kt % C::kStages, ci = kt / 2, cs = ci % C::kCodeStages;
             wait(&s_cfull[cs], (ci / C::kCodeStages) & 1);
-            const uint8_t* cp = codes + cs * C::kCodes + at;
-            uint4 v[2 * kHalves];
+            const uint8_t* cp = codes + cs * C::kCodes + r * 128;
+            uint4 v[4];
 #pragma unroll
-            for (int i = 0; i < 2 * kHalves; ++i) v[i] = *reinterpret_cast<const uint4*>(cp + ((kt % kPerCodes * 2 * kHalves + i) ^ (r & 7)) * 16);
+            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(cp + ((kt % 2 * 4 + i) ^ (r & 7)) * 16);
             if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
-            uint8_t* ap = stages + s * (C::kA + C::kB) + at;
+            tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < 2 * kHalves; ++i) {
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            for (int i = 0; i < 4; ++i) {
                 const uint32_t z2 = Z ? (0x4300u | (z_now >> ((k + 32 * i) % kSpan / G * 8) & 0xffu)) * 0x10001u : 0x43084308u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4*>(ap + i / 2 * (128 * 128) + ((i % 2 * 4 + j) ^ (r & 7)) * 16) =
-                        convert8(w[j], Z ? 0u : 0x08080808u, z2);
+                uint32_t w[16];
+                convert8(v[i].x, Z ? 0u : 0x08080808u, z2, w);
+                convert8(v[i].y, Z ? 0u : 0x08080808u, z2, w + 4);
+                convert8(v[i].z, Z ? 0u : 0x08080808u, z2, w + 8);
+                convert8(v[i].w, Z ? 0u : 0x08080808u, z2, w + 12);
+                tmem_st_x16(to + s * 64 + i * 16, w);
             }
-            fence_proxy_async_smem();
+            tmem_st_wait();
+            tc_fence_before();
             mbar_arrive(&s_full[s]);
-            if (kt % kPerCodes / 2 == kPerCodes / 2 - 1) mbar_arrive(&s_cempty[cs]);
+            if (kParts == 2 || kt % 2 == 1) mbar_arrive(&s_cempty[cs]);
         }
     } else {
-        if constexpr (NTOK > 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");   // 5 warpgroups of 96 at launch: 3 x 40 + 2 x 176
-        const int erow = (warp % 4) * 32 + lane, ecol = (warp - 4 - C::kConvert) / 4 * C::kCols;
-        float total[C::kCols];
+        if constexpr (NTOK == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        if constexpr (NTOK == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        const int erow = (warp % 4) * 32 + lane, ecol = (warp - 4 - C::kConvert) / 4 * C::kCols;    // in every pass
+        float total[C::kPasses * C::kCols];
         const int64_t srow = ((int64_t)e * a.d_out + min(n0 + erow, a.d_out - 1)) * groups;
 #pragma unroll
-        for (int i = 0; i < C::kCols; ++i) total[i] = 0.0f;
+        for (int i = 0; i < C::kPasses * C::kCols; ++i) total[i] = 0.0f;
         const int g0 = k_begin / G, g1 = k_end / G;
-        const auto add = [&](uint32_t (&v)[16], int c, float sc) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) total[c + i] = fmaf(sc, __uint_as_float(v[i]), total[c + i]);
-        };
         uint32_t now[kGroups], next[kGroups];
         load_scales(next, a.scales, srow + g0, groups - g0, scale_f32, vec);
+        int n = 0;                       // passes done
         for (int gs = g0; gs < g1; gs += kGroups) {
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) now[i] = next[i];
             if (gs + kGroups < g1) load_scales(next, a.scales, srow + gs + kGroups, groups - gs - kGroups, scale_f32, vec);
+#pragma unroll 1
+            for (int gi = 0; gi < kGroups && gs + gi < g1; ++gi) {
+                float sc = 0.0f;
 #pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi) {
-                if (gs + gi >= g1) break;
-                const float sc = scale_of(now, gi, scale_f32);
-                const int buf = gi % 2;  // a span has an even number of groups
-                wait(&s_afull[buf], ((gs - g0 + gi) / 2) & 1);
-                tc_fence_after();
-                const uint32_t from = tmem + buf * NTOK + ecol + ((uint32_t)(warp % 4 * 32) << 16);
-                uint32_t v0[16], v1[16];     // a load runs while the other's values are added
-                if (ecol < n_pad) tmem_ld_x16(from, v0);
+                for (int i = 0; i < kGroups; ++i)
+                    if (i == gi) sc = scale_of(now, i, scale_f32);
 #pragma unroll
-                for (int c = 0; c < C::kCols; c += 32) {
-                    tmem_ld_wait();
-                    if (ecol + c + 16 < n_pad) tmem_ld_x16(from + c + 16, v1);
-                    if (ecol + c < n_pad) add(v0, c, sc);
-                    tmem_ld_wait();
-                    if (c + 32 < C::kCols && ecol + c + 32 < n_pad) tmem_ld_x16(from + c + 32, v0);
-                    if (ecol + c + 16 < n_pad) add(v1, c + 16, sc);
+                for (int p = 0; p < C::kPasses; ++p) {
+                    if (p >= n_pass) break;
+                    const int buf = n % 2, cols = n_pad - p * C::kPassCols - ecol;   // of this warp's, from its first on
+                    wait(&s_afull[buf], (n / 2) & 1);
+                    ++n;
+                    tc_fence_after();
+                    const uint32_t from = tmem + buf * C::kPassCols + ecol + ((uint32_t)(warp % 4 * 32) << 16);
+                    if constexpr (NTOK == 256) {     // four warps a scheduler hide each other's loads
+#pragma unroll
+                        for (int c = 0; c < C::kCols; c += 16) {
+                            if (c >= cols) break;
+                            uint32_t v[16];
+                            tmem_ld_x16(from + c, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                total[p * C::kCols + c + i] = fmaf(sc, __uint_as_float(v[i]), total[p * C::kCols + c + i]);
+                        }
+                    } else {
+                        uint32_t v[2][16];           // a load runs while the other's values are added
+                        if (cols > 0) tmem_ld_x16(from, v[0]);
+#pragma unroll
+                        for (int c = 0; c < C::kCols; c += 16) {
+                            tmem_ld_wait();
+                            if (c + 16 < C::kCols && c + 16 < cols) tmem_ld_x16(from + c + 16, v[c / 16 % 2 ^ 1]);
+                            if (c < cols) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    total[c + i] = fmaf(sc, __uint_as_float(v[c / 16 % 2][i]), total[c + i]);
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_aempty[buf]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_aempty[buf]);
             }
         }
+        const auto token = [&](int i) { return i / C::kCols * C::kPassCols + ecol + i % C::kCols; };
         if (n_split > 1) {               // the last group's MMAs are complete, and so are all before them
 #pragma unroll
-            for (int i = 0; i < C::kCols; ++i) red[(ecol + i) * C::kRedStride + erow] = total[i];
+            for (int i = 0; i < C::kPasses * C::kCols; ++i) red[token(i) * C::kRedStride + erow] = total[i];
         } else if (!*abort_flag && n0 + erow < a.d_out) {
 #pragma unroll
-            for (int i = 0; i < C::kCols; ++i)
-                if (ecol + i < n_tok && s_xrow[ecol + i] >= 0) {
-                    const int64_t to = (int64_t)(row0 + ecol + i) * a.ldy + n0 + erow;
+            for (int i = 0; i < C::kPasses * C::kCols; ++i)
+                if (token(i) < n_tok && s_xrow[token(i)] >= 0) {
+                    const int64_t to = (int64_t)(row0 + token(i)) * a.ldy + n0 + erow;
                     if (y_f32) static_cast<float*>(a.y)[to] = total[i];
                     else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(total[i]));
                 }
@@ -411,7 +462,7 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     }
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * NTOK);
+        tmem_dealloc(tmem, C::kTmem);
     }
 }
 
