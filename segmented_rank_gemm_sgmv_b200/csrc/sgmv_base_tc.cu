@@ -18,30 +18,33 @@ namespace {
 // exact in bf16, as its A operand and x as B, and sums one group of K values at a time into tensor memory; the
 // epilogue warps fetch each group's sums and add them, times the row's fp32 scale, to totals in registers, so that
 // no scale is ever rounded to bf16.  The converted codes go straight to tensor memory (a thread holds a row, which is
-// a lane there): through shared memory they made its bandwidth the bound, at 61 % of the MMA rate.  There is room
-// for two accumulators of 128 columns beside them, so 256 rows of x take two passes over each group's K values.
+// a lane there): through shared memory they made its bandwidth the bound, at 61 % of the MMA rate.
+//
+// Everything that hands an accumulator over (waits, fences, the issue of 8 MMAs) takes about 1000 cycles, as long as
+// the MMAs of 128 x 256 x 128.  So there are two lanes, each an MMA warp, an accumulator of at most 128 columns and a
+// set of epilogue warps: with more than 128 rows of x they take half of the rows each, else alternate groups, whose
+// totals are added at the end.
 //
 // What bounds it: with 256 rows of x, shared memory (x written and read once, 1152 cycles for 128 K values) and the
-// tensor cores (1024); with groups of 32, the epilogue; with few rows, the conversion and the stream of codes.
+// tensor cores (1024); with groups of 32 and with few rows, the handing over, the conversion and the stream of codes.
 //
-// Roles: warp 0 streams codes (TMA, stages of 128 rows x 256 values), 1 issues the MMAs, 2 copies x (TMA), 4 or 8
-// warps convert (of 8, half take each stage), the rest are the epilogue, many where a pass leaves them little time.  K is split over the CTAs of a cluster when there are
-// few tiles; their totals meet in shared memory in a fixed order.
+// Roles: warp 0 streams codes (TMA, stages of 128 rows x 256 values), 2 copies x (TMA), 1 and 3 issue the MMAs, 4 or 8
+// warps convert (of 8, half take each stage), the rest are the epilogue.  K is split over the CTAs of a cluster when
+// there are few tiles.  All totals meet in shared memory in a fixed order.
 template <int NTOK>
 struct TcConfig {
     static constexpr int kConvert = NTOK == 256 ? 4 : 8;             // warps
-    static constexpr int kEpilogue = NTOK <= 64 ? 4 : NTOK == 128 ? 8 : 16;
+    static constexpr int kEpilogue = NTOK == 256 ? 16 : 8;
     static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
     static constexpr int kPassCols = NTOK < 128 ? NTOK : 128;        // columns of an accumulator
-    static constexpr int kPasses = NTOK / kPassCols;
-    static constexpr int kCols = kPassCols / (kEpilogue / 4);        // of them, an epilogue warp's
+    static constexpr int kCols = kPassCols / (kEpilogue / 8);        // of them, an epilogue warp's
     static constexpr int kStages = NTOK <= 64 ? 4 : 3;               // of 128 K values
     static constexpr int kCodeStages = NTOK == 256 ? 2 : 3;          // of 256 K values
     static constexpr int kB = NTOK * 256, kCodes = 128 * 128;
     static constexpr int kSmem = 1024 + kStages * kB + kCodeStages * kCodes;
     static constexpr int kTmemA = 2 * kPassCols, kTmem = kTmemA + kStages * 64 <= 256 ? 256 : 512;    // columns
-    static constexpr int kRedStride = 132;                           // floats of a row of x in the cluster's sum
-    static_assert(NTOK * kRedStride * 4 <= kSmem - 1024, "the totals fit into the operands' memory");
+    static constexpr int kRedStride = 132;                           // floats of a row of totals
+    static_assert(2 * kPassCols * kRedStride * 4 <= kSmem - 1024, "the totals fit into the operands' memory");
     static_assert(kSmem <= 227 * 1024 && kTmemA + kStages * 64 <= 512, "the stages fit");
 };
 constexpr int kTcRows = 128, kStageK = 128;
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     const int c0 = (int)((int64_t)all * rank / n_split), c1 = (int)((int64_t)all * (rank + 1) / n_split);
     const int k_begin = c0 * 256, k_end = min(a.d_in, c1 * 256), n_k = (k_end - k_begin + kStageK - 1) / kStageK;
     const int n_pad = (n_tok + 15) / 16 * 16;    // columns of the MMAs
-    const int n_pass = (n_pad + C::kPassCols - 1) / C::kPassCols;
+    const bool halves = n_pad > C::kPassCols;    // the lanes take half of the rows each, else alternate groups
     const int groups = a.d_in / G;
 
     if (tid < NTOK) {
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&s_full[i], 128 + 1);
-            mbar_init(&s_empty[i], 1);
+            mbar_init(&s_empty[i], 2);
         }
         for (int i = 0; i < C::kCodeStages; ++i) {
             mbar_init(&s_cfull[i], 1);
@@ -224,9 +227,9 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_afull[i], 1);
-            mbar_init(&s_aempty[i], C::kEpilogue);
+            mbar_init(&s_aempty[i], C::kEpilogue / 2);
         }
-        mbar_init(&s_done, 1);
+        mbar_init(&s_done, 2);
         s_abort = 0;
         fence_mbar_init();
     }
@@ -250,13 +253,13 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
             }
     };
 
-    float* red = reinterpret_cast<float*>(stages);                   // the CTA's totals, for its cluster
+    float* red = reinterpret_cast<float*>(stages);                   // [2 kPassCols][kRedStride] totals
 
     int n_x = 0;                         // stages of x asked for
     if (warp < 4) {
         // 5 warpgroups of 96 registers at launch: 48 + 2 x 56 + 2 x 160; or 6 of 80: 40 + 56 + 4 x 96
-        if constexpr (NTOK == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if constexpr (NTOK == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 0) {
             if (lane == 0) {
                 int i = 0;
@@ -270,40 +273,40 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
                 for (int j = max(0, i - C::kCodeStages); j < i; ++j)         // no copy is left in flight
                     mbar_wait(&s_cfull[j % C::kCodeStages], (j / C::kCodeStages) & 1, &g_err_base_tc);
             }
-        } else if (warp == 1) {
-            const uint64_t bdesc = smem_desc_sw128(smem_u32(stages), 16, 1024);
-            int n = 0, s = 0;            // passes begun; the stage's slot
+        } else if (warp == 1 || warp == 3) {
+            const int ln = warp / 2;     // 0 or 1
+            const uint64_t bdesc = smem_desc_sw128(smem_u32(stages), 16, 1024) + (halves ? ln * (C::kPassCols * 128 / 16) : 0);
+            const uint32_t idesc = idesc_bf16_f32(128, halves ? (ln ? n_pad - C::kPassCols : C::kPassCols) : n_pad, false, false);
+            const uint32_t d = tmem + ln * C::kPassCols;
+            int n = 0, s = 0, g = 0;     // this lane's groups begun; the stage's slot; groups
             for (int kt = 0; kt < n_k; ++kt) {
                 wait(&s_full[s], (kt / C::kStages) & 1);
                 tc_fence_after();
                 const int n_groups = min(kStageK, k_end - k_begin - kt * kStageK) / G;
+                const uint32_t at = tmem + C::kTmemA + s * 64;
+                const uint64_t bd = bdesc + (uint64_t)(s * (C::kB / 16));
 #pragma unroll
                 for (int gi = 0; gi < kStageK / G; ++gi) {
                     if (gi >= n_groups) break;
-#pragma unroll
-                    for (int p = 0; p < C::kPasses; ++p) {
-                        if (p >= n_pass) break;
-                        const int buf = n % 2;
-                        if (n >= 2) {
-                            wait(&s_aempty[buf], (n / 2 - 1) & 1);
-                            tc_fence_after();
-                        }
-                        ++n;
-                        if (elect_one()) {
-                            const uint32_t idesc = idesc_bf16_f32(128, min(C::kPassCols, n_pad - p * C::kPassCols), false, false);
-                            const uint32_t d = tmem + buf * C::kPassCols, at = tmem + C::kTmemA + s * 64;
-                            const uint64_t bd = bdesc + (uint64_t)((s * C::kB + p * (C::kPassCols * 128)) / 16);
-#pragma unroll
-                            for (int i = 0; i < G / 16; ++i) {
-                                const int ks = gi * (G / 16) + i;
-                                tc_mma_bf16_ts(d, at + ks * 8, bd + (ks / 4) * (NTOK * 128 / 16) + ks % 4 * 2, idesc, i > 0);
-                            }
-                            tc_commit(&s_afull[buf]);
-                            if (gi == n_groups - 1 && p == n_pass - 1) tc_commit(&s_empty[s]);
-                        }
-                        __syncwarp();
+                    if (!halves && (g + gi) % 2 != ln) continue;
+                    if (n > 0) {
+                        wait(&s_aempty[ln], (n - 1) & 1);
+                        tc_fence_after();
                     }
+                    ++n;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < G / 16; ++i) {
+                            const int ks = gi * (G / 16) + i;
+                            tc_mma_bf16_ts(d, at + ks * 8, bd + (ks / 4) * (NTOK * 128 / 16) + ks % 4 * 2, idesc, i > 0);
+                        }
+                        tc_commit(&s_afull[ln]);
+                    }
+                    __syncwarp();
                 }
+                g += n_groups;
+                if (elect_one()) tc_commit(&s_empty[s]);     // arrives at once where this lane had no group
+                __syncwarp();
                 s = s == C::kStages - 1 ? 0 : s + 1;
             }
             if (elect_one()) tc_commit(&s_done);     // no MMA is left in flight
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp < 4 + C::kConvert) {
-        if constexpr (NTOK > 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; of two sets of warps each takes alternate stages
         constexpr int kParts = C::kConvert / 4;
         const int64_t zrow = ((int64_t)e * a.d_out + min(n0 + r, a.d_out - 1)) * groups;
@@ -366,97 +369,85 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
             if (kParts == 2 || kt % 2 == 1) mbar_arrive(&s_cempty[cs]);
         }
     } else {
-        if constexpr (NTOK == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         if constexpr (NTOK == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
-        const int erow = (warp % 4) * 32 + lane, ecol = (warp - 4 - C::kConvert) / 4 * C::kCols;    // in every pass
-        float total[C::kPasses * C::kCols];
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        const int ew = warp - 4 - C::kConvert, ln = ew / (C::kEpilogue / 2);
+        const int erow = (warp % 4) * 32 + lane, ecol = ew % (C::kEpilogue / 2) / 4 * C::kCols;     // of the lane's accumulator
+        const int cols = (halves ? (ln ? n_pad - C::kPassCols : C::kPassCols) : n_pad) - ecol;      // of this warp's that are used
+        float total[C::kCols];
         const int64_t srow = ((int64_t)e * a.d_out + min(n0 + erow, a.d_out - 1)) * groups;
 #pragma unroll
-        for (int i = 0; i < C::kPasses * C::kCols; ++i) total[i] = 0.0f;
+        for (int i = 0; i < C::kCols; ++i) total[i] = 0.0f;
         const int g0 = k_begin / G, g1 = k_end / G;
         uint32_t now[kGroups], next[kGroups];
         load_scales(next, a.scales, srow + g0, groups - g0, scale_f32, vec);
-        int n = 0;                       // passes done
+        int n = 0;                       // groups done
         for (int gs = g0; gs < g1; gs += kGroups) {
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) now[i] = next[i];
             if (gs + kGroups < g1) load_scales(next, a.scales, srow + gs + kGroups, groups - gs - kGroups, scale_f32, vec);
-#pragma unroll 1
-            for (int gi = 0; gi < kGroups && gs + gi < g1; ++gi) {
-                float sc = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i)
-                    if (i == gi) sc = scale_of(now, i, scale_f32);
+            for (int gi = 0; gi < kGroups; ++gi) {
+                if (gs + gi >= g1) break;
+                if (!halves && gi % 2 != ln) continue;               // a span begins at an even group
+                const float sc = scale_of(now, gi, scale_f32);
+                wait(&s_afull[ln], n++ & 1);
+                tc_fence_after();
+                const uint32_t from = tmem + ln * C::kPassCols + ecol + ((uint32_t)(warp % 4 * 32) << 16);
 #pragma unroll
-                for (int p = 0; p < C::kPasses; ++p) {
-                    if (p >= n_pass) break;
-                    const int buf = n % 2, cols = n_pad - p * C::kPassCols - ecol;   // of this warp's, from its first on
-                    wait(&s_afull[buf], (n / 2) & 1);
-                    ++n;
-                    tc_fence_after();
-                    const uint32_t from = tmem + buf * C::kPassCols + ecol + ((uint32_t)(warp % 4 * 32) << 16);
-                    if constexpr (NTOK == 256) {     // four warps a scheduler hide each other's loads
+                for (int c = 0; c < C::kCols; c += 32) {
+                    if (c >= cols) break;
+                    uint32_t v0[16], v1[16];
+                    tmem_ld_x16(from + c, v0);
+                    if (C::kCols > 16) tmem_ld_x16(from + c + 16, v1);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < C::kCols; c += 16) {
-                            if (c >= cols) break;
-                            uint32_t v[16];
-                            tmem_ld_x16(from + c, v);
-                            tmem_ld_wait();
+                    for (int i = 0; i < 16; ++i) total[c + i] = fmaf(sc, __uint_as_float(v0[i]), total[c + i]);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                total[p * C::kCols + c + i] = fmaf(sc, __uint_as_float(v[i]), total[p * C::kCols + c + i]);
-                        }
-                    } else {
-                        uint32_t v[2][16];           // a load runs while the other's values are added
-                        if (cols > 0) tmem_ld_x16(from, v[0]);
-#pragma unroll
-                        for (int c = 0; c < C::kCols; c += 16) {
-                            tmem_ld_wait();
-                            if (c + 16 < C::kCols && c + 16 < cols) tmem_ld_x16(from + c + 16, v[c / 16 % 2 ^ 1]);
-                            if (c < cols) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    total[c + i] = fmaf(sc, __uint_as_float(v[c / 16 % 2][i]), total[c + i]);
-                            }
-                        }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_aempty[buf]);
+                    for (int i = 0; i < 16; ++i) total[c + 16 + i] = fmaf(sc, __uint_as_float(v1[i]), total[c + 16 + i]);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_aempty[ln]);
             }
         }
-        const auto token = [&](int i) { return i / C::kCols * C::kPassCols + ecol + i % C::kCols; };
-        if (n_split > 1) {               // the last group's MMAs are complete, and so are all before them
+        named_bar_sync(1, C::kEpilogue * 32);        // both lanes' last MMAs are complete: the totals take the stages' memory
 #pragma unroll
-            for (int i = 0; i < C::kPasses * C::kCols; ++i) red[token(i) * C::kRedStride + erow] = total[i];
-        } else if (!*abort_flag && n0 + erow < a.d_out) {
-#pragma unroll
-            for (int i = 0; i < C::kPasses * C::kCols; ++i)
-                if (token(i) < n_tok && s_xrow[token(i)] >= 0) {
-                    const int64_t to = (int64_t)(row0 + token(i)) * a.ldy + n0 + erow;
-                    if (y_f32) static_cast<float*>(a.y)[to] = total[i];
-                    else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(total[i]));
-                }
-        }
+        for (int i = 0; i < C::kCols; ++i)
+            if (i < cols) red[(ln * C::kPassCols + ecol + i) * C::kRedStride + erow] = total[i];
     }
     __syncthreads();                     // every copy and MMA is complete: each was waited for
-    if (n_split > 1) {                   // the CTAs' totals, in a fixed order
-        cluster_sync();
-        const uint32_t base = smem_u32(red);
-        for (int i = rank * C::kThreads + tid; i < n_tok * 128; i += n_split * C::kThreads) {
-            const int t = i / 128, n = i % 128;
-            float v[8];
+    // the totals of the lanes and of the cluster's CTAs, in a fixed order
+    if (n_split > 1) cluster_sync();
+    const uint32_t base = smem_u32(red);
+    for (int i = rank * C::kThreads + tid; i < n_tok * 128; i += n_split * C::kThreads) {
+        const int t = i / 128, n = i % 128;
+        float v;
+        if (n_split == 1) {
+            v = red[t * C::kRedStride + n];
+            if (!halves) v += red[(C::kPassCols + t) * C::kRedStride + n];
+        } else {
+            float u[8], w[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = c < n_split ? ld_cluster_f32(map_cluster(base + (t * C::kRedStride + n) * 4, c)) : 0.0f;
-#pragma unroll
-            for (int c = 1; c < 8; ++c) v[0] += v[c];
-            if (n0 + n < a.d_out && s_xrow[t] >= 0 && !*abort_flag) {
-                const int64_t to = (int64_t)(row0 + t) * a.ldy + n0 + n;
-                if (y_f32) static_cast<float*>(a.y)[to] = v[0];
-                else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+            for (int c = 0; c < 8; ++c) {
+                u[c] = w[c] = 0.0f;
+                if (c < n_split) {
+                    const uint32_t from = map_cluster(base, c);
+                    u[c] = ld_cluster_f32(from + (t * C::kRedStride + n) * 4);
+                    if (!halves) w[c] = ld_cluster_f32(from + ((C::kPassCols + t) * C::kRedStride + n) * 4);
+                }
             }
+            v = u[0] + w[0];
+#pragma unroll
+            for (int c = 1; c < 8; ++c) v += u[c] + w[c];
         }
+        if (n0 + n < a.d_out && s_xrow[t] >= 0 && !*abort_flag) {
+            const int64_t to = (int64_t)(row0 + t) * a.ldy + n0 + n;
+            if (y_f32) static_cast<float*>(a.y)[to] = v;
+            else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        }
+    }
+    if (n_split > 1) {
         cluster_arrive_relaxed();        // every CTA of the cluster has read the totals
         cluster_wait_acquire();
     }
