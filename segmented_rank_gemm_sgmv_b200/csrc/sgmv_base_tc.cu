@@ -31,14 +31,14 @@ namespace {
 // Roles: warp 0 streams codes (TMA, stages of 128 rows x 256 values), 2 copies x (TMA), 1 and 3 issue the MMAs, 4 or 8
 // warps convert (of 8, half take each stage), the rest are the epilogue.  K is split over the CTAs of a cluster when
 // there are few tiles.  All totals meet in shared memory in a fixed order.
-template <int NTOK>
+template <int G, int NTOK>
 struct TcConfig {
-    static constexpr int kConvert = NTOK == 256 ? 4 : 8;             // warps
+    static constexpr int kConvert = NTOK == 256 ? 4 : NTOK == 128 || G < 128 ? 8 : 16;       // warps
     static constexpr int kEpilogue = NTOK == 256 ? 16 : 8;
     static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
     static constexpr int kPassCols = NTOK < 128 ? NTOK : 128;        // columns of an accumulator
     static constexpr int kCols = kPassCols / (kEpilogue / 8);        // of them, an epilogue warp's
-    static constexpr int kStages = NTOK <= 64 ? 4 : 3;               // of 128 K values
+    static constexpr int kStages = NTOK <= 64 ? 6 : 3;               // of 128 K values
     static constexpr int kCodeStages = NTOK == 256 ? 2 : 3;          // of 256 K values
     static constexpr int kB = NTOK * 256, kCodes = 128 * 128;
     static constexpr int kSmem = 1024 + kStages * kB + kCodeStages * kCodes;
@@ -143,10 +143,10 @@ __device__ __forceinline__ void convert8(uint32_t c, uint32_t flip, uint32_t z2,
 }
 
 template <int G, int NTOK, bool Z>
-__global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
+__global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
     base_tc_kernel(BaseArgs a, const __grid_constant__ CUtensorMap codes_map,
                    const __grid_constant__ CUtensorMap x_map, bool scale_f32, bool y_f32, bool vec, int n_split) {
-    using C = TcConfig<NTOK>;
+    using C = TcConfig<G, NTOK>;
     constexpr int kSpan = G == 32 ? 128 : 256, kGroups = kSpan / G;  // K values whose scales are loaded together
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages], s_cfull[C::kCodeStages], s_cempty[C::kCodeStages],
@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     const int k_begin = c0 * 256, k_end = min(a.d_in, c1 * 256), n_k = (k_end - k_begin + kStageK - 1) / kStageK;
     const int n_pad = (n_tok + 15) / 16 * 16;    // columns of the MMAs
     const bool halves = n_pad > C::kPassCols;    // the lanes take half of the rows each, else alternate groups
+    const bool alone = !halves && G == kStageK;  // then each stage is one lane's
     const int groups = a.d_in / G;
 
     if (tid < NTOK) {
@@ -219,11 +220,11 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&s_full[i], 128 + 1);
-            mbar_init(&s_empty[i], 2);
+            mbar_init(&s_empty[i], alone ? 1 : 2);
         }
         for (int i = 0; i < C::kCodeStages; ++i) {
             mbar_init(&s_cfull[i], 1);
-            mbar_init(&s_cempty[i], C::kConvert * 32);
+            mbar_init(&s_cempty[i], C::kConvert == 4 ? 128 : 256);           // the threads that read a stage
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_afull[i], 1);
@@ -257,11 +258,12 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
 
     int n_x = 0;                         // stages of x asked for
     if (warp < 4) {
-        // 5 warpgroups of 96 registers at launch: 48 + 2 x 56 + 2 x 160; or 6 of 80: 40 + 56 + 4 x 96
-        if constexpr (NTOK == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        // registers at launch: 7 warpgroups of 72 = 40 + 4 x 56 + 2 x 120; 5 of 96 = 48 + 2 x 56 + 2 x 160; 6 of 80 =
+        // 40 + 56 + 4 x 96
+        if constexpr (C::kConvert == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
-            if (lane == 0) {
+            if (elect_one()) {
                 int i = 0;
                 for (; i < c1 - c0; ++i) {
                     const int s = i % C::kCodeStages;
@@ -278,8 +280,9 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
             const uint64_t bdesc = smem_desc_sw128(smem_u32(stages), 16, 1024) + (halves ? ln * (C::kPassCols * 128 / 16) : 0);
             const uint32_t idesc = idesc_bf16_f32(128, halves ? (ln ? n_pad - C::kPassCols : C::kPassCols) : n_pad, false, false);
             const uint32_t d = tmem + ln * C::kPassCols;
-            int n = 0, s = 0, g = 0;     // this lane's groups begun; the stage's slot; groups
-            for (int kt = 0; kt < n_k; ++kt) {
+            int n = 0, g = 0;            // this lane's groups begun; the stage's first group
+            for (int kt = alone ? ln : 0; kt < n_k; kt += alone ? 2 : 1) {
+                const int s = kt % C::kStages;
                 wait(&s_full[s], (kt / C::kStages) & 1);
                 tc_fence_after();
                 const int n_groups = min(kStageK, k_end - k_begin - kt * kStageK) / G;
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
 #pragma unroll
                 for (int gi = 0; gi < kStageK / G; ++gi) {
                     if (gi >= n_groups) break;
-                    if (!halves && (g + gi) % 2 != ln) continue;
+                    if (!halves && !alone && (g + gi) % 2 != ln) continue;
                     if (n > 0) {
                         wait(&s_aempty[ln], (n - 1) & 1);
                         tc_fence_after();
@@ -307,12 +310,12 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
                 g += n_groups;
                 if (elect_one()) tc_commit(&s_empty[s]);     // arrives at once where this lane had no group
                 __syncwarp();
-                s = s == C::kStages - 1 ? 0 : s + 1;
             }
             if (elect_one()) tc_commit(&s_done);     // no MMA is left in flight
             mbar_wait(&s_done, 0, &g_err_base_tc);
-        } else {
-            for (int kt = 0; warp == 2 && lane == 0 && kt < n_k; ++kt) {
+        } else if (warp == 2) {
+            const bool copier = elect_one();
+            for (int kt = 0; copier && kt < n_k; ++kt) {
                 const int s = kt % C::kStages;
                 if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
                 if (*abort_flag) break;
@@ -366,11 +369,12 @@ __global__ void __launch_bounds__(TcConfig<NTOK>::kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&s_full[s]);
-            if (kParts == 2 || kt % 2 == 1) mbar_arrive(&s_cempty[cs]);
+            if (kParts > 1 || kt % 2 == 1) mbar_arrive(&s_cempty[cs]);
         }
     } else {
         if constexpr (NTOK == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        else if constexpr (C::kConvert == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int ew = warp - 4 - C::kConvert, ln = ew / (C::kEpilogue / 2);
         const int erow = (warp % 4) * 32 + lane, ecol = ew % (C::kEpilogue / 2) / 4 * C::kCols;     // of the lane's accumulator
         const int cols = (halves ? (ln ? n_pad - C::kPassCols : C::kPassCols) : n_pad) - ecol;      // of this warp's that are used
@@ -490,7 +494,7 @@ cudaError_t encode_x(CUtensorMap* map, const BaseArgs& a, int rows) {
 
 template <int G, int NTOK, bool Z>
 cudaError_t launch_t(const BaseArgs& a, bool scale_f32, bool y_f32, cudaStream_t stream) {
-    using C = TcConfig<NTOK>;
+    using C = TcConfig<G, NTOK>;
     auto kern = base_tc_kernel<G, NTOK, Z>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (err != cudaSuccess) return err;
