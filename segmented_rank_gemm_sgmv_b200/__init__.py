@@ -686,30 +686,40 @@ def lora_delta(x: torch.Tensor, plan: BatchPlan, pool: AdapterPool, y: torch.Ten
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 
+# The checks run on every call of kernels that take a few microseconds: messages are made only on failure.
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
 
 
-def _mat(t: torch.Tensor, name: str, device) -> Tuple[int, int]:
+def _here(t: torch.Tensor, name: str) -> int:
+    """The device index of `t`, which has to be the current CUDA device."""
+    d = t.get_device()
+    _need(d >= 0 and d == torch.cuda.current_device(), f"{name} must be on the current CUDA device")
+    return d
+
+
+def _mat(t: torch.Tensor, name: str, device: int) -> Tuple[int, int]:
     """(address, row stride) of a bf16 or fp32 matrix on `device` whose rows are contiguous."""
-    _need(t.dtype in _DTYPE and t.dim() == 2 and t.device == device, f"{name} must be a bf16 or fp32 matrix on {device}")
+    if t.dtype not in _DTYPE or t.dim() != 2 or t.get_device() != device:
+        raise ValueError(f"{name} must be a bf16 or fp32 matrix on cuda:{device}")
     rows, cols = t.shape
-    _need(cols <= 1 or rows == 0 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else (cols + 7) // 8 * 8)
+    ld, step = t.stride()
+    if step != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), (ld if rows > 1 else (cols + 7) // 8 * 8)
 
 
-def _flat(t: torch.Tensor, name: str, dtype, device) -> int:
+def _flat(t: torch.Tensor, name: str, dtype, device: int) -> int:
     """Address of a contiguous tensor of `dtype` on `device`."""
-    _need(t.dtype == dtype and t.device == device and t.is_contiguous(), f"{name} must be a contiguous {dtype} tensor on {device}")
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}")
     return t.data_ptr()
 
 
-def _here(t: torch.Tensor, name: str):
-    """The device of `t`, which has to be the current CUDA device."""
-    d = t.device
-    _need(d.type == "cuda" and d.index == torch.cuda.current_device(), f"{name} must be on the current CUDA device")
-    return d
+def _on(stream, device: int) -> int:
+    """Handle of `stream`, or of the current stream of `device`."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _record(made, stream) -> None:
@@ -720,7 +730,7 @@ def _record(made, stream) -> None:
             t.record_stream(s)
 
 
-def _weights4(codes, scales, zeros, lead: int, device):
+def _weights4(codes, scales, zeros, lead: int, device: int):
     """Checks and addresses of a 4-bit matrix: codes [.., d_out, d_in / 2], scales and zeros [.., d_out, d_in / group]."""
     pc = _flat(codes, "codes", torch.uint8, device)
     _need(codes.dim() == 2 + lead and scales.dim() == 2 + lead and scales.shape[:-1] == codes.shape[:-1],
@@ -749,8 +759,8 @@ def base_product(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, y: 
     T, d_out = x.shape[0], codes.shape[0]
     _need(x.dtype == torch.bfloat16 and x.shape[1] == d_in, "x must be bf16 [T, d_in]")
     _need(y.shape[0] == T and y.shape[1] == d_out, "y must be [T, d_out]")
-    _check(load_library().sgmv_base_product(px, ldx, T, d_in, d_out, pc, ps, sdt, pz, group, py, ldy, _DTYPE[y.dtype],
-                                            _stream(stream)))
+    _check((_lib or load_library()).sgmv_base_product(px, ldx, T, d_in, d_out, pc, ps, sdt, pz, group, py, ldy, _DTYPE[y.dtype],
+                                            _on(stream, dev)))
     return y
 
 
@@ -770,7 +780,7 @@ def base_product_experts(x: torch.Tensor, codes: torch.Tensor, scales: torch.Ten
     _need(y.shape[1] == d_out, "y must be [rows, d_out]")
     po = _flat(offsets, "offsets", torch.int32, dev)
     _need(offsets.numel() == n_experts + 1, "offsets must have one value per expert and one more")
-    lib = load_library()
+    lib = (_lib or load_library())
     psl, k, pw, need = None, 1, None, 0
     if slot_of is not None:
         psl = _flat(slot_of, "slot_of", torch.int32, dev)
@@ -779,13 +789,13 @@ def base_product_experts(x: torch.Tensor, codes: torch.Tensor, scales: torch.Ten
         k = rows // x_rows if rows else 1
         need = lib.sgmv_base_product_experts_workspace(rows, d_in, n_experts)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
             pw = workspace.data_ptr()
             _record([workspace], stream)
     else:
         _need(x_rows == rows, "x and y must have the same rows without slot_of")
     _check(lib.sgmv_base_product_experts(px, ldx, x_rows, d_in, d_out, n_experts, pc, ps, sdt, pz, group, po, psl, k, rows,
-                                         py, ldy, _DTYPE[y.dtype], pw, max(need, 0), _stream(stream)))
+                                         py, ldy, _DTYPE[y.dtype], pw, max(need, 0), _on(stream, dev)))
     return y
 
 
@@ -799,38 +809,38 @@ def expert_order(expert_ids: torch.Tensor, n_experts: int, offsets: Optional[tor
     pi = _flat(expert_ids, "expert_ids", torch.int32, dev)
     _need(expert_ids.dim() == 2, "expert_ids must be [T, k]")
     T, k = expert_ids.shape
-    lib = load_library()
+    lib = (_lib or load_library())
     made = []
     if offsets is None:
-        offsets = torch.empty(max(int(n_experts), 0) + 1, dtype=torch.int32, device=dev)
+        offsets = torch.empty(max(int(n_experts), 0) + 1, dtype=torch.int32, device=expert_ids.device)
         made.append(offsets)
     if row_of is None:
         row_of = torch.empty_like(expert_ids)
         made.append(row_of)
     if slot_of is None:
-        slot_of = torch.empty(T * k, dtype=torch.int32, device=dev)
+        slot_of = torch.empty(T * k, dtype=torch.int32, device=expert_ids.device)
         made.append(slot_of)
     _need(offsets.numel() == n_experts + 1 and row_of.shape == expert_ids.shape and slot_of.numel() == T * k,
           "offsets, row_of and slot_of must have n_experts + 1, [T, k] and T * k values")
     need = lib.sgmv_expert_order_workspace(T, k, n_experts)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=expert_ids.device)
         made.append(workspace)
     _record(made, stream)
     pw, nw = (None, 0) if workspace is None else (_flat(workspace, "workspace", workspace.dtype, dev),
                                                   workspace.numel() * workspace.element_size())
     _check(lib.sgmv_expert_order(pi, T, k, n_experts, _flat(offsets, "offsets", torch.int32, dev),
                                  _flat(row_of, "row_of", torch.int32, dev), _flat(slot_of, "slot_of", torch.int32, dev),
-                                 pw, nw, _stream(stream)))
+                                 pw, nw, _on(stream, dev)))
     return offsets, row_of, slot_of
 
 
 def expert_order_workspace(T: int, k: int, n_experts: int) -> int:
     """Bytes of workspace that expert_order takes for these sizes (-1: refused sizes)."""
-    return int(load_library().sgmv_expert_order_workspace(int(T), int(k), int(n_experts)))
+    return int((_lib or load_library()).sgmv_expert_order_workspace(int(T), int(k), int(n_experts)))
 
 
-def _rows_of(row_of: torch.Tensor, device) -> Tuple[int, int, int]:
+def _rows_of(row_of: torch.Tensor, device: int) -> Tuple[int, int, int]:
     _need(row_of.dim() == 2, "row_of must be [T, k]")
     return _flat(row_of, "row_of", torch.int32, device), row_of.shape[0], row_of.shape[1]
 
@@ -843,8 +853,8 @@ def expert_gather(x: torch.Tensor, row_of: torch.Tensor, xs: torch.Tensor, strea
     px, ldx = _mat(x, "x", dev)
     ps, lds = _mat(xs, "xs", dev)
     _need(x.dtype == xs.dtype and x.shape[0] == T and x.shape[1] == xs.shape[1], "x [T, d] and xs [rows, d] must have one dtype and d")
-    _check(load_library().sgmv_expert_gather(px, ldx, T, x.shape[1], _DTYPE[x.dtype], pr, k, ps, lds, xs.shape[0],
-                                             _stream(stream)))
+    _check((_lib or load_library()).sgmv_expert_gather(px, ldx, T, x.shape[1], _DTYPE[x.dtype], pr, k, ps, lds, xs.shape[0],
+                                             _on(stream, dev)))
     return xs
 
 
@@ -855,8 +865,8 @@ def expert_gather_backward(dxs: torch.Tensor, row_of: torch.Tensor, dx: torch.Te
     ps, lds = _mat(dxs, "dxs", dev)
     px, ldx = _mat(dx, "dx", dev)
     _need(dx.dtype == dxs.dtype and dx.shape[0] == T and dx.shape[1] == dxs.shape[1], "dx [T, d] and dxs [rows, d] must have one dtype and d")
-    _check(load_library().sgmv_expert_gather_backward(ps, lds, dxs.shape[0], T, dx.shape[1], _DTYPE[dx.dtype], pr, k, px,
-                                                      ldx, _stream(stream)))
+    _check((_lib or load_library()).sgmv_expert_gather_backward(ps, lds, dxs.shape[0], T, dx.shape[1], _DTYPE[dx.dtype], pr, k, px,
+                                                      ldx, _on(stream, dev)))
     return dx
 
 
@@ -877,8 +887,8 @@ def expert_combine(ys: torch.Tensor, row_of: torch.Tensor, y: torch.Tensor, weig
     if add is not None:
         pa, lda = _mat(add, "add", dev)
         _need(add.shape == y.shape and add.dtype == y.dtype, "add must have the shape and dtype of y")
-    _check(load_library().sgmv_expert_combine(ps, lds, ys.shape[0], _DTYPE[ys.dtype], pr, pw, T, k, y.shape[1], pa, lda,
-                                              py, ldy, _DTYPE[y.dtype], _stream(stream)))
+    _check((_lib or load_library()).sgmv_expert_combine(ps, lds, ys.shape[0], _DTYPE[ys.dtype], pr, pw, T, k, y.shape[1], pa, lda,
+                                              py, ldy, _DTYPE[y.dtype], _on(stream, dev)))
     return y
 
 
@@ -904,6 +914,6 @@ def expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, row_of: torch.Te
     if dweights is not None:
         pdw = _flat(dweights, "dweights", torch.float32, dev)
         _need(dweights.shape == row_of.shape, "dweights must have the shape of row_of")
-    _check(load_library().sgmv_expert_combine_backward(pd, ldd, _DTYPE[dy.dtype], ps, lds, ys.shape[0], _DTYPE[ys.dtype],
-                                                       pr, pw, T, k, dy.shape[1], pg, ldg, pdw, _stream(stream)))
+    _check((_lib or load_library()).sgmv_expert_combine_backward(pd, ldd, _DTYPE[dy.dtype], ps, lds, ys.shape[0], _DTYPE[ys.dtype],
+                                                       pr, pw, T, k, dy.shape[1], pg, ldg, pdw, _on(stream, dev)))
     return dys, dweights
