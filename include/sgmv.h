@@ -607,19 +607,28 @@ SGMV_API sgmv_status sgmv_lora_delta_noalloc(const void* x, int64_t ldx, int32_t
  *          two's complement, -8..7; with zeros it is unsigned, 0..15.
  * scales   device [d_out][d_in / group], scale_dtype 0 = bf16, 1 = fp32
  * zeros    device uint8 [d_out][d_in / group], each 0..15, or NULL
- * group    32, 64 or 128 values; d_in is a multiple of it, at most 524288
+ * group    32, 64 or 128 values; d_in is a multiple of it, at most 2^20
  * x        device bf16 [T][ldx], ldx >= d_in, row starts 16-byte aligned
  * y        device [T][ldy], ldy >= d_out, y_dtype 0 = bf16, 1 = fp32; aligned to
  *          its type.  It is written, not accumulated into, and may not overlap x.
- * T >= 0 and d_out >= 1 are any.  The products are exact in fp32 (codes and x
- * are bf16 values), summed in fp32, the scale applied in fp32 per group and the
- * result rounded once; the order of the sum is fixed for given sizes, so a call
- * repeats bit for bit.  The pointers belong to the current device.
+ * workspace device, 16-byte aligned, of the bytes sgmv_base_product_workspace
+ *          gives (0: may be NULL); nothing in it is kept from call to call, but
+ *          two calls that may overlap need two
+ * T is 0..2^23 and d_out >= 1 any.  Sums are held in fp32 or exact integers, the
+ * scale is applied in fp32 per group and the result rounded once.  From 17 rows on
+ * the products (codes less zero points, times x) are exact.  Below, a row of x is
+ * held in fixed point of 2^-22 of its largest value's binade, so that values down
+ * to 2^-14 of the largest are exact and smaller ones off by at most 2^-23 of it.
+ * The order of the sum is fixed for given sizes: a call repeats bit for bit.  The
+ * pointers belong to the current device.
  */
 SGMV_API sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, int32_t d_in, int32_t d_out,
                                        const void* codes, const void* scales, int32_t scale_dtype,
                                        const uint8_t* zeros, int32_t group, void* y, int64_t ldy,
-                                       int32_t y_dtype, sgmv_stream_t stream);
+                                       int32_t y_dtype, void* workspace, int64_t workspace_bytes,
+                                       sgmv_stream_t stream);
+/* Bytes of workspace of a call (0: none; -1: refused sizes). */
+SGMV_API int64_t sgmv_base_product_workspace(int32_t T, int32_t d_in, int32_t group);
 /*
  * The same with one matrix per expert: codes, scales and zeros have a leading
  * dimension n_experts (1..4096), and row i of y, offsets[e] <= i < offsets[e+1],
@@ -628,9 +637,7 @@ SGMV_API sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, in
  * offsets  device int32 [n_experts + 1], ascending from 0, last <= rows
  * slot_of  device int32 [rows] (sgmv_expert_order), or NULL; k: choices per token
  * rows     rows of y; x_rows: rows of x (>= rows without slot_of)
- * workspace device, 16-byte aligned, for calls with slot_of: the bytes that
- *          sgmv_base_product_experts_workspace gives (0: may be NULL); nothing in
- *          it is kept, but two calls that may overlap need two
+ * workspace as above, of the bytes sgmv_base_product_experts_workspace gives
  * Rows of y from offsets[n_experts] on are left as they were.  A slot whose
  * token is not a row of x is reported by sgmv_check_errors and its row left
  * unwritten; offsets that do not ascend from 0 to at most rows are reported, and
@@ -642,8 +649,9 @@ SGMV_API sgmv_status sgmv_base_product_experts(const void* x, int64_t ldx, int32
                                                int32_t group, const int32_t* offsets, const int32_t* slot_of,
                                                int32_t k, int32_t rows, void* y, int64_t ldy, int32_t y_dtype,
                                                void* workspace, int64_t workspace_bytes, sgmv_stream_t stream);
-/* Bytes of workspace of a call with slot_of (0: none; -1: refused sizes). */
-SGMV_API int64_t sgmv_base_product_experts_workspace(int32_t rows, int32_t d_in, int32_t n_experts);
+/* Bytes of workspace of a call, with or without slot_of (0: none; -1: refused sizes). */
+SGMV_API int64_t sgmv_base_product_experts_workspace(int32_t rows, int32_t d_in, int32_t group,
+                                                     int32_t n_experts, int32_t with_slots);
 
 /* ------------------------------------------------------------------------ */
 /* Tokens sorted by expert and back                                          */

@@ -39,7 +39,7 @@ EXPORTED = ("sgmv_status_string", "sgmv_last_error", "sgmv_pool_create", "sgmv_p
             "sgmv_lora_delta_host",
             "sgmv_check_errors", "sgmv_residency_create", "sgmv_residency_destroy",
             "sgmv_residency_register", "sgmv_residency_unregister", "sgmv_residency_prepare",
-            "sgmv_residency_get_stats", "sgmv_base_product", "sgmv_base_product_experts",
+            "sgmv_residency_get_stats", "sgmv_base_product", "sgmv_base_product_workspace", "sgmv_base_product_experts",
             "sgmv_base_product_experts_workspace",
             "sgmv_expert_order_workspace", "sgmv_expert_order", "sgmv_expert_gather", "sgmv_expert_gather_backward",
             "sgmv_expert_combine", "sgmv_expert_combine_backward")
@@ -139,10 +139,11 @@ def load_library() -> ctypes.CDLL:
         "sgmv_residency_unregister": (st, [vp, i32]),
         "sgmv_residency_prepare": (st, [vp, vp, i32, vp, vp, ctypes.POINTER(i32)]),
         "sgmv_residency_get_stats": (st, [vp, ctypes.POINTER(ResidencyStats)]),
-        "sgmv_base_product": (st, [vp, i64, i32, i32, i32, vp, vp, i32, vp, i32, vp, i64, i32, vp]),
+        "sgmv_base_product": (st, [vp, i64, i32, i32, i32, vp, vp, i32, vp, i32, vp, i64, i32, vp, i64, vp]),
+        "sgmv_base_product_workspace": (i64, [i32, i32, i32]),
         "sgmv_base_product_experts": (st, [vp, i64, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, i32, i32, vp,
                                            i64, i32, vp, i64, vp]),
-        "sgmv_base_product_experts_workspace": (i64, [i32, i32, i32]),
+        "sgmv_base_product_experts_workspace": (i64, [i32, i32, i32, i32, i32]),
         "sgmv_expert_order_workspace": (i64, [i32, i32, i32]),
         "sgmv_expert_order": (st, [vp, i32, i32, i32, vp, vp, vp, vp, i64, vp]),
         "sgmv_expert_gather": (st, [vp, i64, i32, i32, i32, vp, i32, vp, i64, i32, vp]),
@@ -730,6 +731,15 @@ def _record(made, stream) -> None:
             t.record_stream(s)
 
 
+def _workspace(need: int, like: torch.Tensor, stream) -> Optional[int]:
+    """Address of `need` bytes from torch's allocator, of the current stream, for work on `stream`."""
+    if need <= 0:
+        return None
+    w = torch.empty(need, dtype=torch.uint8, device=like.device)
+    _record([w], stream)
+    return w.data_ptr()
+
+
 def _weights4(codes, scales, zeros, lead: int, device: int):
     """Checks and addresses of a 4-bit matrix: codes [.., d_out, d_in / 2], scales and zeros [.., d_out, d_in / group]."""
     pc = _flat(codes, "codes", torch.uint8, device)
@@ -759,8 +769,11 @@ def base_product(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, y: 
     T, d_out = x.shape[0], codes.shape[0]
     _need(x.dtype == torch.bfloat16 and x.shape[1] == d_in, "x must be bf16 [T, d_in]")
     _need(y.shape[0] == T and y.shape[1] == d_out, "y must be [T, d_out]")
-    _check((_lib or load_library()).sgmv_base_product(px, ldx, T, d_in, d_out, pc, ps, sdt, pz, group, py, ldy, _DTYPE[y.dtype],
-                                            _on(stream, dev)))
+    lib = _lib or load_library()
+    need = lib.sgmv_base_product_workspace(T, d_in, group)
+    pw = _workspace(need, x, stream)
+    _check(lib.sgmv_base_product(px, ldx, T, d_in, d_out, pc, ps, sdt, pz, group, py, ldy, _DTYPE[y.dtype], pw, need,
+                                 _on(stream, dev)))
     return y
 
 
@@ -780,22 +793,19 @@ def base_product_experts(x: torch.Tensor, codes: torch.Tensor, scales: torch.Ten
     _need(y.shape[1] == d_out, "y must be [rows, d_out]")
     po = _flat(offsets, "offsets", torch.int32, dev)
     _need(offsets.numel() == n_experts + 1, "offsets must have one value per expert and one more")
-    lib = (_lib or load_library())
-    psl, k, pw, need = None, 1, None, 0
+    psl, k = None, 1
     if slot_of is not None:
         psl = _flat(slot_of, "slot_of", torch.int32, dev)
         _need(slot_of.numel() == rows and (rows % x_rows == 0 if x_rows else rows == 0),
               "slot_of must have a slot for every row of y, k for every row of x")
         k = rows // x_rows if rows else 1
-        need = lib.sgmv_base_product_experts_workspace(rows, d_in, n_experts)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-            pw = workspace.data_ptr()
-            _record([workspace], stream)
     else:
         _need(x_rows == rows, "x and y must have the same rows without slot_of")
+    lib = _lib or load_library()
+    need = lib.sgmv_base_product_experts_workspace(rows, d_in, group, n_experts, psl is not None)
+    pw = _workspace(need, x, stream)
     _check(lib.sgmv_base_product_experts(px, ldx, x_rows, d_in, d_out, n_experts, pc, ps, sdt, pz, group, po, psl, k, rows,
-                                         py, ldy, _DTYPE[y.dtype], pw, max(need, 0), _on(stream, dev)))
+                                         py, ldy, _DTYPE[y.dtype], pw, need, _on(stream, dev)))
     return y
 
 

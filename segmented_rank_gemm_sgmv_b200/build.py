@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libsgmv_b200.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["sgmv_api.cu", "sgmv_pool.cu", "sgmv_plan.cpp", "sgmv_simt.cu", "sgmv_tc.cu", "sgmv_experts.cu", "sgmv_base.cu",
-           "sgmv_base_tc.cu"]
+           "sgmv_base_i8.cu", "sgmv_base_tc.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]

@@ -9,7 +9,8 @@
 namespace sgmv {
 
 constexpr int kMaxExperts = 4096;      // experts of one order / one base product
-constexpr int kMaxBaseK = 524288;      // d_in of a base product: x of one row fits into a cluster
+constexpr int kMaxBaseK = 1 << 20;     // d_in of a base product
+constexpr int kMaxBaseRows = 1 << 23;  // rows of a base product: its units fit into a grid
 constexpr int kMaxExpertsPerToken = 64;
 constexpr int64_t kMaxSlots = 1 << 30; // token-expert slots of one order
 
@@ -19,6 +20,7 @@ enum : uint32_t { kErrExpert = 16u };  // expert id or expert offset out of rang
 // Read and clear the device error words of the translation units.
 cudaError_t read_clear_errors_experts(uint32_t* bits, cudaStream_t stream);
 cudaError_t read_clear_errors_base(uint32_t* bits, cudaStream_t stream);
+cudaError_t read_clear_errors_base_i8(uint32_t* bits, cudaStream_t stream);
 cudaError_t read_clear_errors_base_tc(uint32_t* bits, cudaStream_t stream);
 
 // y = W x for rows of 4-bit codes; see sgmv_base_product in include/sgmv.h.
@@ -35,7 +37,10 @@ struct BaseArgs {
     int32_t rows, x_rows, k, experts, d_in, d_out, group;
 };
 
-// The tcgen05 kernel for many rows (sgmv_base_tc.cu); `per`: rows of a matrix, on average.
+// The kernels for few rows (sgmv_base_i8.cu; with its workspace) and for many (sgmv_base_tc.cu).  `per`: rows of a
+// matrix, on average.
+int64_t base_i8_workspace(int64_t rows, int64_t d_in, int64_t group);
+cudaError_t launch_base_i8(const BaseArgs& a, int64_t per, bool scale_f32, bool y_f32, void* workspace, cudaStream_t stream);
 cudaError_t launch_base_tc(const BaseArgs& a, int64_t per, bool scale_f32, bool y_f32, cudaStream_t stream);
 
 }  // namespace sgmv

@@ -661,6 +661,7 @@ extern "C" sgmv_status sgmv_check_errors(sgmv_stream_t stream_, uint32_t* flags)
     SGMV_CUDA_TRY(read_clear_errors_tc(&bits, stream));
     SGMV_CUDA_TRY(read_clear_errors_experts(&bits, stream));
     SGMV_CUDA_TRY(read_clear_errors_base(&bits, stream));
+    SGMV_CUDA_TRY(read_clear_errors_base_i8(&bits, stream));
     SGMV_CUDA_TRY(read_clear_errors_base_tc(&bits, stream));
     if (flags) *flags = bits;
     if (bits & kErrTimeout) return fail(SGMV_ERR_TIMEOUT, "a device-side wait timed out");

@@ -1,0 +1,503 @@
+// Base products from 4-bit weights for few rows of x: integer tensor cores on x in 24-bit fixed point.
+#include <algorithm>
+
+#include "base_tc.cuh"
+
+namespace sgmv {
+
+__device__ unsigned int g_err_base_i8;
+
+namespace {
+
+// y^T = W x^T in tiles of 128 rows of W and up to TT rows of x.
+//
+// With few rows of x the stream of codes should be the bound, and what stands in its way is turning codes into
+// tensor-core operands: to bf16, eight codes take 13 operations.  To bytes they take 3.  So a first kernel writes each
+// row of x in fixed point, X = x 2^(21 - E) rounded to an integer, |X| <= 2^22, E the exponent of the row's largest
+// value, as three signed digits of base 256, and tcgen05.mma (kind i8) multiplies the codes, 0..15, by the digits: a
+// group's sums are exact integers.  The epilogue takes z times the digits' sums from them, still exactly, joins the
+// digits in fp32 (hi = 256 a_2 + a_1 in 27 bits, then 256 hi + a_0 rounded once) and adds them, times the row's fp32
+// scale, to the total, which is multiplied by 2^(E - 21) at the end.
+//
+// The one rounding of x: values down to 2^-14 of the row's largest are exact (bf16 has 8 bits), smaller ones are off by
+// at most half a unit, 2^-23 of it, which is what an fp32 sum that holds the largest value rounds to.  A row that holds
+// an infinity or a NaN has no E: its outputs are summed in fp32 from the codes themselves, as the formula says.
+//
+// The digits' K order inside eight values is 0 2 4 6 1 3 5 7: the even and the odd nibbles of a word of codes are two
+// words of bytes.  The codes go to tensor memory as the A operand (a thread a row, a lane a row), three planes of
+// digits are the B operand: columns d TT + t.  Two lanes (MMA warp, accumulator, epilogue warps) take alternate groups.
+// K is split over the CTAs of a cluster; two CTAs share an SM.
+//
+// Roles: warp 0 streams codes (TMA), 2 copies digits (TMA), 1 and 3 issue the MMAs, 8 warps convert (half of them each
+// stage), 8 are the epilogue.
+template <int TT>
+struct I8Config {
+    static constexpr int kConvert = 8, kEpilogue = 8;                // warps
+    static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
+    static constexpr int kCols = TT == 8 ? 32 : 48;                  // columns of an MMA: 3 TT, a multiple of 16
+    static constexpr int kStages = TT == 8 ? 6 : 5;                  // of 128 K values
+    static constexpr int kCodeStages = 3;                            // of 256 K values
+    static constexpr int kB = kCols * 128, kBCopied = 3 * TT * 128, kCodes = 128 * 128;
+    static constexpr int kTmemA = 2 * kCols, kTmem = 256;            // columns
+    static constexpr int kRedStride = 132;                           // floats of a row of totals
+    static constexpr int kSmem = 1024 + kStages * kB + kCodeStages * kCodes;
+    static_assert(kTmemA + kStages * 32 <= kTmem, "the stages fit");
+    static_assert(2 * TT * kRedStride * 4 <= kCodeStages * kCodes, "the totals fit into the codes' memory");
+};
+constexpr int kNotFinite = 0x7fffffff;                               // in place of an exponent
+
+// What the first kernel writes, in the workspace.
+struct Digits {
+    int8_t* digits;            // [3][rows][d_in]
+    int2* sums;                // [groups][rows]: 256 S_2 + S_1 and S_0, the sums of a group's digits
+    int32_t* exponent;         // [rows]: E - 21, or kNotFinite
+};
+
+// 3-plane digits of each row of y's x.  A block a row: its largest magnitude, then its digits, 8 values a thread.
+__global__ void __launch_bounds__(1024) base_digits_kernel(BaseArgs a, Digits o, int group) {
+    pdl_launch_dependents();
+    const int r = blockIdx.x, units = a.d_in / 8;
+    int xr = r;
+    if (a.offsets && r >= a.offsets[a.experts]) return;              // a row of no expert
+    if (a.slot_of) {
+        const int slot = a.slot_of[r];
+        xr = slot / a.k;
+        if (slot < 0 || xr >= a.x_rows) {
+            if (threadIdx.x == 0) atomicOr(&g_err_base_i8, kErrRows);
+            return;
+        }
+    }
+    const uint4* x = reinterpret_cast<const uint4*>(a.x + (int64_t)xr * a.ldx);
+    // magnitudes of bf16 values compare as integers; an exponent of 255 is an infinity or a NaN
+    uint32_t most = 0;
+    for (int u = threadIdx.x; u < units; u += blockDim.x) {
+        const uint4 v = x[u];
+        most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+    most = max(most & 0xffffu, most >> 16);
+    most = __reduce_max_sync(0xffffffffu, most);
+    __shared__ uint32_t s_most[32];
+    if (threadIdx.x % 32 == 0) s_most[threadIdx.x / 32] = most;
+    __syncthreads();
+    most = threadIdx.x % 32 < blockDim.x / 32 ? s_most[threadIdx.x % 32] : 0;
+    most = __reduce_max_sync(0xffffffffu, most);
+    const bool finite = most < 0x7f80u;
+    // largest value < 2^(E + 1); below the normal range E = -126 serves, whose units are finer than the values'
+    const int e = max((int)(most >> 7), 1) - 127;
+    if (threadIdx.x == 0) o.exponent[r] = finite ? e - 21 : kNotFinite;
+    if (!finite) return;                 // the digits are not used
+    const int steps = (units + blockDim.x - 1) / blockDim.x;
+    for (int i = 0; i < steps; ++i) {
+        const int u = i * blockDim.x + threadIdx.x;
+        float f[8] = {};
+        if (u < units) unpack8(x[u], f);
+        uint32_t plane[3][2] = {};
+        int s1 = 0, s0 = 0, s2 = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int X = __float2int_rn(scalbnf(f[j], 21 - e));
+            const int d0 = (int8_t)X, X1 = (X - d0) >> 8, d1 = (int8_t)X1, d2 = (X1 - d1) >> 8;
+            const int at = j % 2, shift = j / 2 * 8;
+            plane[0][at] |= (uint32_t)(d0 & 0xff) << shift;
+            plane[1][at] |= (uint32_t)(d1 & 0xff) << shift;
+            plane[2][at] |= (uint32_t)(d2 & 0xff) << shift;
+            s0 += d0;
+            s1 += d1;
+            s2 += d2;
+        }
+        if (u < units)
+#pragma unroll
+            for (int d = 0; d < 3; ++d)
+                *reinterpret_cast<uint2*>(o.digits + ((int64_t)d * a.rows + r) * a.d_in + u * 8) = make_uint2(plane[d][0], plane[d][1]);
+        int hi = 256 * s2 + s1;
+        for (int k = 1; k < group / 8; k *= 2) {                     // a group's 4, 8 or 16 units are neighbouring lanes
+            hi += __shfl_xor_sync(0xffffffffu, hi, k);
+            s0 += __shfl_xor_sync(0xffffffffu, s0, k);
+        }
+        if (u < units && u % (group / 8) == 0) o.sums[(int64_t)(u / (group / 8)) * a.rows + r] = make_int2(hi, s0);
+    }
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T on bytes, A unsigned and B signed, to int32: A has a lane a row and four consecutive
+// K values a column.
+__device__ __forceinline__ void tc_mma_i8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+// Instruction descriptor for kind::i8 with unsigned A, signed B and int32 D.
+__host__ __device__ constexpr uint32_t idesc_u8_s8(int M, int N) { return (2u << 4) | (0u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
+
+template <int G, int TT, bool Z>
+__global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
+    base_i8_kernel(BaseArgs a, Digits in, const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap digits_map,
+                   bool scale_f32, bool y_f32, bool vec, int n_split) {
+    using C = I8Config<TT>;
+    constexpr int kSpan = G == 32 ? 128 : 256, kGroups = kSpan / G;  // K values whose scales are loaded together
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages], s_cfull[C::kCodeStages], s_cempty[C::kCodeStages],
+        s_afull[2], s_aempty[2], s_done;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ int2 s_sums[C::kEpilogue][TT];
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
+    const int rank = blockIdx.x % n_split, n0 = (int)(blockIdx.x / n_split) * kTcRows;
+    uint8_t* stages = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;  // [kStages][kCols] rows of 128 digits
+    uint8_t* codes = stages + C::kStages * C::kB;                            // [kCodeStages][128] rows of 256 codes
+
+    // the unit: up to TT consecutive rows of y of one matrix
+    int e = 0, row0 = blockIdx.y * TT, row_end = min(a.rows, (int)(blockIdx.y + 1) * TT);
+    if (a.offsets && !find_unit<C::kThreads>(a, TT, &g_err_base_i8, &e, &row0, &row_end)) return;
+    const int n_tok = row_end - row0;
+
+    // this CTA's code stages of K and operand stages
+    const int all = (a.d_in + kCodesK - 1) / kCodesK;
+    const int c0 = (int)((int64_t)all * rank / n_split), c1 = (int)((int64_t)all * (rank + 1) / n_split);
+    const int k_begin = c0 * kCodesK, k_end = min(a.d_in, c1 * kCodesK), n_k = (k_end - k_begin + kStageK - 1) / kStageK;
+    const int groups = a.d_in / G;
+    constexpr bool kAlone = G == kStageK;                            // each stage is one lane's
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&s_full[i], 128 + 1);
+            mbar_init(&s_empty[i], kAlone ? 1 : 2);
+        }
+        for (int i = 0; i < C::kCodeStages; ++i) {
+            mbar_init(&s_cfull[i], 1);
+            mbar_init(&s_cempty[i], 256);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_afull[i], 1);
+            mbar_init(&s_aempty[i], C::kEpilogue / 2);
+        }
+        mbar_init(&s_done, 2);
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&s_tmem, C::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+    // waits give up together: whoever runs out of time stops the others' waits too
+    volatile int* abort_flag = &s_abort;
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, parity) && !*abort_flag)
+            if (clock64() - t0 > kWaitLimitCycles) {
+                atomicOr(&g_err_base_i8, kErrTimeout);
+                *abort_flag = 1;
+            }
+    };
+    float* red = reinterpret_cast<float*>(codes);                    // [2 TT][kRedStride] totals
+
+    // registers at launch: 5 warpgroups of 48 = 40 + 2 x 40 + 2 x 56 and some
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {
+            if (elect_one()) {           // the codes are not the first kernel's: they need not wait for it
+                int i = 0;
+                for (; i < c1 - c0; ++i) {
+                    const int s = i % C::kCodeStages;
+                    if (i >= C::kCodeStages) wait(&s_cempty[s], (i / C::kCodeStages - 1) & 1);
+                    if (*abort_flag) break;
+                    mbar_arrive_expect_tx(&s_cfull[s], C::kCodes);
+                    tma_load_3d(codes + s * C::kCodes, &codes_map, (c0 + i) * (kCodesK / 2), n0, e, &s_cfull[s]);
+                }
+                for (int j = max(0, i - C::kCodeStages); j < i; ++j)         // no copy is left in flight
+                    mbar_wait(&s_cfull[j % C::kCodeStages], (j / C::kCodeStages) & 1, &g_err_base_i8);
+            }
+        } else if (warp == 2) {
+            pdl_wait();
+            if (elect_one()) {
+                int kt = 0;
+                for (; kt < n_k; ++kt) {
+                    const int s = kt % C::kStages;
+                    if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
+                    if (*abort_flag) break;
+                    mbar_arrive_expect_tx(&s_full[s], C::kBCopied);
+#pragma unroll
+                    for (int d = 0; d < 3; ++d)
+                        tma_load_3d(stages + s * C::kB + d * TT * 128, &digits_map, k_begin + kt * kStageK, row0, d, &s_full[s]);
+                }
+                if (*abort_flag)         // no copy is left in flight
+                    for (int j = max(0, kt - C::kStages); j < kt; ++j) mbar_wait(&s_full[j % C::kStages], (j / C::kStages) & 1, &g_err_base_i8);
+            }
+        } else {
+            const int ln = warp / 2;     // 0 or 1
+            const uint64_t bdesc = smem_desc_sw128(smem_u32(stages), 16, 1024);
+            const uint32_t d = tmem + ln * C::kCols;
+            constexpr uint32_t idesc = idesc_u8_s8(128, C::kCols);
+            int n = 0, g = 0;            // this lane's groups begun; the stage's first group
+            for (int kt = kAlone ? ln : 0; kt < n_k; kt += kAlone ? 2 : 1) {
+                const int s = kt % C::kStages;
+                wait(&s_full[s], (kt / C::kStages) & 1);
+                tc_fence_after();
+                const int n_groups = min(kStageK, k_end - k_begin - kt * kStageK) / G;
+                const uint32_t at = tmem + C::kTmemA + s * 32;
+                const uint64_t bd = bdesc + (uint64_t)(s * (C::kB / 16));
+#pragma unroll
+                for (int gi = 0; gi < kStageK / G; ++gi) {
+                    if (gi >= n_groups) break;
+                    if (!kAlone && (g + gi) % 2 != ln) continue;
+                    if (n > 0) {
+                        wait(&s_aempty[ln], (n - 1) & 1);
+                        tc_fence_after();
+                    }
+                    ++n;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < G / 32; ++i) {
+                            const int ks = gi * (G / 32) + i;
+                            tc_mma_i8_ts(d, at + ks * 8, bd + ks * 2, idesc, i > 0);
+                        }
+                        tc_commit(&s_afull[ln]);
+                    }
+                    __syncwarp();
+                }
+                g += n_groups;
+                if (elect_one()) tc_commit(&s_empty[s]);     // arrives at once where this lane had no group
+                __syncwarp();
+            }
+            if (elect_one()) tc_commit(&s_done);     // no MMA is left in flight
+            mbar_wait(&s_done, 0, &g_err_base_i8);
+        }
+        __syncwarp();
+    } else if (warp < 4 + C::kConvert) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; of two sets of warps each takes alternate stages
+        const uint32_t to = tmem + C::kTmemA + ((uint32_t)(warp % 4 * 32) << 16);
+        constexpr uint32_t kFlip = Z ? 0u : 0x08080808u;             // two's complement codes to excess 8
+        for (int kt = part; kt < n_k; kt += 2) {
+            const int s = kt % C::kStages, ci = kt / 2, cs = ci % C::kCodeStages;
+            wait(&s_cfull[cs], (ci / C::kCodeStages) & 1);
+            const uint8_t* cp = codes + cs * C::kCodes + r * 128;
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(cp + ((kt % 2 * 4 + i) ^ (r & 7)) * 16);
+            if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t c[8] = {v[2 * i].x, v[2 * i].y, v[2 * i].z, v[2 * i].w, v[2 * i + 1].x, v[2 * i + 1].y, v[2 * i + 1].z, v[2 * i + 1].w};
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    w[2 * j] = (c[j] & 0x0f0f0f0fu) ^ kFlip;
+                    w[2 * j + 1] = ((c[j] >> 4) & 0x0f0f0f0fu) ^ kFlip;
+                }
+                tmem_st_x16(to + s * 32 + i * 16, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&s_full[s]);
+            mbar_arrive(&s_cempty[cs]);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 56;");
+        pdl_wait();
+        const int ew = warp - 4 - C::kConvert, ln = ew / 4;
+        const int erow = (warp % 4) * 32 + lane;
+        float total[TT];
+        const int64_t srow = ((int64_t)e * a.d_out + min(n0 + erow, a.d_out - 1)) * groups;
+#pragma unroll
+        for (int i = 0; i < TT; ++i) total[i] = 0.0f;
+        const int g0 = k_begin / G, g1 = k_end / G;
+        uint32_t now[kGroups], next[kGroups], z_now = 0, z_next = 0;
+        load_scales(next, a.scales, srow + g0, groups - g0, scale_f32, vec);
+        if constexpr (Z) z_next = load_zeros<kGroups>(a.zeros, srow + g0, groups - g0, vec);
+        const auto sums_of = [&](int g) {                            // lane t: row t's sums of group g
+            return g < g1 && lane < n_tok ? in.sums[(int64_t)g * a.rows + row0 + lane] : make_int2(0, 0);
+        };
+        int2 sums = sums_of(g0 + ln);
+        int n = 0;                       // groups done
+        for (int gs = g0; gs < g1; gs += kGroups) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) now[i] = next[i];
+            z_now = z_next;
+            if (gs + kGroups < g1) {
+                load_scales(next, a.scales, srow + gs + kGroups, groups - gs - kGroups, scale_f32, vec);
+                if constexpr (Z) z_next = load_zeros<kGroups>(a.zeros, srow + gs + kGroups, groups - gs - kGroups, vec);
+            }
+#pragma unroll
+            for (int gi = 0; gi < kGroups; ++gi) {
+                if (gs + gi >= g1) break;
+                if (gi % 2 != ln) continue;                          // a span begins at an even group
+                const float sc = scale_of(now, gi, scale_f32);
+                const int z = Z ? (int)(z_now >> (8 * gi) & 0xffu) : 8;
+                if (lane < TT) s_sums[ew][lane] = sums;
+                __syncwarp();
+                sums = sums_of(gs + gi + 2);
+                wait(&s_afull[ln], n++ & 1);
+                tc_fence_after();
+                const uint32_t from = tmem + ln * C::kCols + ((uint32_t)(warp % 4 * 32) << 16);
+#pragma unroll
+                for (int t = 0; t < TT; t += 8) {
+                    if (t >= n_tok) break;
+                    uint32_t d0[8], d1[8], d2[8];
+                    tmem_ld_x8(from + t, d0);
+                    tmem_ld_x8(from + TT + t, d1);
+                    tmem_ld_x8(from + 2 * TT + t, d2);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int2 s = s_sums[ew][t + i];
+                        const int hi = (int)d2[i] * 256 + (int)d1[i] - z * s.x, lo = (int)d0[i] - z * s.y;
+                        total[t + i] = fmaf(sc, fmaf((float)hi, 256.0f, (float)lo), total[t + i]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_aempty[ln]);
+            }
+        }
+        named_bar_sync(1, C::kEpilogue * 32);        // every code has been read: the totals take the codes' memory
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+            if (i < n_tok) red[(ln * TT + i) * C::kRedStride + erow] = total[i];
+    }
+    __syncthreads();                     // every copy and MMA is complete: each was waited for
+    pdl_wait();
+    // the totals of the lanes and of the cluster's CTAs, in a fixed order
+    if (n_split > 1) cluster_sync();
+    const uint32_t base = smem_u32(red);
+    for (int i = rank * C::kThreads + tid; i < n_tok * 128; i += n_split * C::kThreads) {
+        const int t = i / 128, n = i % 128, row = row0 + t;
+        float v = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < n_split; ++c) {
+            const uint32_t from = n_split > 1 ? map_cluster(base, c) : base;
+            v += ld_cluster_f32(from + (t * C::kRedStride + n) * 4) + ld_cluster_f32(from + ((TT + t) * C::kRedStride + n) * 4);
+        }
+        if (n0 + n >= a.d_out || *abort_flag) continue;
+        int xr = row;
+        if (a.slot_of) {
+            const int slot = a.slot_of[row];
+            xr = slot / a.k;
+            if (slot < 0 || xr >= a.x_rows) continue;                // reported by the first kernel
+        }
+        const int exponent = in.exponent[row];
+        if (exponent != kNotFinite) {
+            v = scalbnf(v, exponent);
+        } else {                         // infinities and NaN go their way through the formula
+            const int64_t w = (int64_t)e * a.d_out + n0 + n;
+            const uint16_t* x = a.x + (int64_t)xr * a.ldx;
+            v = 0.0f;
+            for (int g = 0; g < groups; ++g) {
+                const float sc = scale_f32 ? static_cast<const float*>(a.scales)[w * groups + g]
+                                           : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.scales)[w * groups + g] << 16);
+                const int z = Z ? a.zeros[w * groups + g] : 8;
+                float sum = 0.0f;
+                for (int k = g * G; k < (g + 1) * G; ++k) {
+                    const int c = (a.codes[w * (a.d_in / 2) + k / 2] >> (k % 2 * 4) & 15) ^ (Z ? 0 : 8);
+                    sum = fmaf((float)(c - z), __uint_as_float((uint32_t)x[k] << 16), sum);
+                }
+                v = fmaf(sc, sum, v);
+            }
+        }
+        const int64_t at = (int64_t)row * a.ldy + n0 + n;
+        if (y_f32) static_cast<float*>(a.y)[at] = v;
+        else static_cast<uint16_t*>(a.y)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    }
+    if (n_split > 1) {
+        cluster_arrive_relaxed();        // every CTA of the cluster has read the totals
+        cluster_wait_acquire();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmem);
+    }
+}
+
+int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+
+template <int G, int TT, bool Z>
+cudaError_t launch_t(const BaseArgs& a, const Digits& in, bool scale_f32, bool y_f32, cudaStream_t stream) {
+    using C = I8Config<TT>;
+    auto kern = base_i8_kernel<G, TT, Z>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (err != cudaSuccess) return err;
+    CUtensorMap map, digits_map;
+    if ((err = encode_codes(&map, a)) != cudaSuccess) return err;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.d_in, (cuuint64_t)a.rows, 3}, strides[2] = {(cuuint64_t)a.d_in, (cuuint64_t)a.rows * a.d_in};
+    const cuuint32_t box[3] = {kStageK, TT, 1};
+    if ((err = encode_map(&digits_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, in.digits, dims, strides, box)) != cudaSuccess) return err;
+    const int tiles = (a.d_out + kTcRows - 1) / kTcRows, k_stages = (a.d_in + kCodesK - 1) / kCodesK;
+    const int64_t units = a.offsets ? (int64_t)a.rows / TT + std::min(a.rows, a.experts) : ((int64_t)a.rows + TT - 1) / TT;
+    // the split of K that takes the fewest rounds of 2 x 148 CTAs, each counted with some code stages' worth of fixed cost
+    int split = 1;
+    double best = 0;
+    for (int c = 1; c <= std::min(8, k_stages); ++c) {
+        const double cost = (double)((tiles * units * c + 295) / 296) * ((k_stages + c - 1) / c + 6);
+        if (c == 1 || cost < 0.97 * best) best = cost, split = c;
+    }
+    constexpr int kSpan = G == 32 ? 128 : 256;
+    const auto at = [](const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+    const bool vec = a.d_in % kSpan == 0 && at(a.scales, 16) && at(a.zeros, 4);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)units);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, in, map, digits_map, scale_f32, y_f32, vec, split);
+}
+
+template <int G, bool Z>
+cudaError_t launch_g(const BaseArgs& a, int64_t per, const Digits& in, bool scale_f32, bool y_f32, cudaStream_t stream) {
+    return per <= 8 ? launch_t<G, 8, Z>(a, in, scale_f32, y_f32, stream) : launch_t<G, 16, Z>(a, in, scale_f32, y_f32, stream);
+}
+
+}  // namespace
+
+int64_t base_i8_workspace(int64_t rows, int64_t d_in, int64_t group) {
+    return round16(3 * rows * d_in) + round16(rows * (d_in / group) * 8) + round16(rows * 4);
+}
+
+cudaError_t launch_base_i8(const BaseArgs& a, int64_t per, bool scale_f32, bool y_f32, void* workspace, cudaStream_t stream) {
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    const int64_t rows = a.rows;
+    const Digits in{reinterpret_cast<int8_t*>(w), reinterpret_cast<int2*>(w + round16(3 * rows * a.d_in)),
+                    reinterpret_cast<int32_t*>(w + round16(3 * rows * a.d_in) + round16(rows * (a.d_in / a.group) * 8))};
+    const int threads = std::min(1024, std::max(32, (a.d_in / 8 + 31) / 32 * 32));
+    base_digits_kernel<<<(unsigned)a.rows, threads, 0, stream>>>(a, in, a.group);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (a.zeros)
+        return a.group == 128  ? launch_g<128, true>(a, per, in, scale_f32, y_f32, stream)
+               : a.group == 64 ? launch_g<64, true>(a, per, in, scale_f32, y_f32, stream)
+                               : launch_g<32, true>(a, per, in, scale_f32, y_f32, stream);
+    return a.group == 128  ? launch_g<128, false>(a, per, in, scale_f32, y_f32, stream)
+           : a.group == 64 ? launch_g<64, false>(a, per, in, scale_f32, y_f32, stream)
+                           : launch_g<32, false>(a, per, in, scale_f32, y_f32, stream);
+}
+
+cudaError_t read_clear_errors_base_i8(uint32_t* bits, cudaStream_t stream) {
+    unsigned int h = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&h, g_err_base_i8, sizeof(h), 0, cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_err_base_i8, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    *bits |= h;
+    return e;
+}
+
+}  // namespace sgmv

@@ -2,11 +2,7 @@
 #include <algorithm>
 #include <cstring>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "experts.h"
-#include "ptx.cuh"
+#include "base_tc.cuh"
 
 namespace sgmv {
 
@@ -47,31 +43,6 @@ struct TcConfig {
     static_assert(2 * kPassCols * kRedStride * 4 <= kSmem - 1024, "the totals fit into the operands' memory");
     static_assert(kSmem <= 227 * 1024 && kTmemA + kStages * 64 <= 512, "the stages fit");
 };
-constexpr int kTcRows = 128, kStageK = 128;
-
-__device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* map, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_u32(dst_smem)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // D[tmem] (+)= A[tmem] * B[smem]^T: A has a lane a row and two consecutive K values a column.
 __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, bool accumulate) {
     asm volatile(
@@ -80,51 +51,6 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
-}
-
-// One lane of a converged warp.  MMAs under this election have their operands in uniform registers; under a branch on
-// the lane number each took about 200 cycles to issue, elected one by one about 100.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-    return ok != 0;
-}
-
-// The scales or zero points of N consecutive groups of a row, as loaded; `left`: groups of the row from the first on,
-// `vec`: at least N, aligned to their size.
-template <int N>
-__device__ __forceinline__ void load_scales(uint32_t (&w)[N], const void* scales, int64_t at, int left, bool f32, bool vec) {
-    if (vec) {
-        if constexpr (N == 2) {
-            if (f32) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(static_cast<const uint32_t*>(scales) + at);
-            else w[0] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(scales) + at);
-        } else {
-            if (f32) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(scales) + at);
-            else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(scales) + at);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < left) {
-            if (f32) w[i] = static_cast<const uint32_t*>(scales)[at + i];
-            else w[i / 2] |= (uint32_t)static_cast<const uint16_t*>(scales)[at + i] << (i % 2 * 16);
-        }
-}
-template <int N>
-__device__ __forceinline__ float scale_of(const uint32_t (&w)[N], int i, bool f32) {
-    return f32 ? __uint_as_float(w[i]) : i % 2 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
-}
-template <int N>
-__device__ __forceinline__ uint32_t load_zeros(const uint8_t* zeros, int64_t at, int left, bool vec) {
-    if (vec) return N == 2 ? *reinterpret_cast<const uint16_t*>(zeros + at) : *reinterpret_cast<const uint32_t*>(zeros + at);
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < left) w |= (uint32_t)zeros[at + i] << (8 * i);
-    return w;
 }
 
 // Eight codes (value i in bits 4i..4i+3) less the zero point, as eight bf16 in order.  bf16 128 + n has the bits
@@ -153,7 +79,6 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
         s_afull[2], s_aempty[2], s_done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_xrow[NTOK];         // -1: the row of y is not written
-    __shared__ int s_unit[3];
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
     const int rank = blockIdx.x % n_split, n0 = (int)(blockIdx.x / n_split) * kTcRows;
@@ -161,42 +86,9 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
     uint8_t* codes = stages + C::kStages * C::kB;                            // [kCodeStages][128] rows of 256 codes
 
     // the unit: up to NTOK consecutive rows of y of one matrix
-    if (a.offsets) {
-        if (warp == 0) {                 // unit number blockIdx.y of the experts' units in order
-            int before = 0, found = 0, bad = 0;
-            for (int e0 = 0; e0 < a.experts && !found; e0 += 32) {
-                const int e = e0 + lane;
-                const int lo = e < a.experts ? a.offsets[e] : 0, hi = e < a.experts ? a.offsets[e + 1] : 0;
-                bad |= e < a.experts && (lo < 0 || hi < lo || hi > a.rows || (e == 0 && lo != 0));
-                const int first = max(lo, 0), end = min(hi, a.rows);
-                const int units = end > first ? (end - first + NTOK - 1) / NTOK : 0;
-                int upto = units;
-#pragma unroll
-                for (int o = 1; o < 32; o *= 2) {
-                    const int v = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += v;
-                }
-                const int k = (int)blockIdx.y - (before + upto - units);
-                if (k >= 0 && k < units) {       // an expert's rows in units of even size
-                    s_unit[0] = e;
-                    s_unit[1] = first + (int)((int64_t)(end - first) * k / units);
-                    s_unit[2] = first + (int)((int64_t)(end - first) * (k + 1) / units);
-                }
-                found = __any_sync(0xffffffffu, k >= 0 && k < units);
-                before += __shfl_sync(0xffffffffu, upto, 31);
-            }
-            if (bad && blockIdx.x == 0) atomicOr(&g_err_base_tc, kErrExpert);
-            if (!found && lane == 0) s_unit[1] = s_unit[2] = s_unit[0] = 0;
-        }
-    } else if (tid == 0) {
-        s_unit[0] = 0;
-        s_unit[1] = blockIdx.y * NTOK;
-        s_unit[2] = min(a.rows, (int)(blockIdx.y + 1) * NTOK);
-    }
-    __syncthreads();
-    const int e = s_unit[0], row0 = s_unit[1], n_tok = s_unit[2] - row0;
-    if (n_tok <= 0) return;              // the same for every CTA of the cluster
-
+    int e = 0, row0 = blockIdx.y * NTOK, row_end = min(a.rows, (int)(blockIdx.y + 1) * NTOK);
+    if (a.offsets && !find_unit<C::kThreads>(a, NTOK, &g_err_base_tc, &e, &row0, &row_end)) return;
+    const int n_tok = row_end - row0;
     // this CTA's code stages of K (256 values) and operand stages (128)
     const int all = (a.d_in + 255) / 256;
     const int c0 = (int)((int64_t)all * rank / n_split), c1 = (int)((int64_t)all * (rank + 1) / n_split);
@@ -461,35 +353,11 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
     }
 }
 
-// A tensor map with the 128-byte swizzle; what lies past an end reads as 0.
-cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
-                   const cuuint32_t* box) {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void* f = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    if (!fn) return cudaErrorNotSupported;
-    const cuuint32_t es[3] = {1, 1, 1};
-    return fn(map, type, rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
-}
-// The codes, [experts][d_out][d_in / 2] bytes, in boxes of 128 rows of 128 bytes.
-cudaError_t encode_codes(CUtensorMap* map, const BaseArgs& a) {
-    const cuuint64_t row_bytes = a.d_in / 2;
-    const cuuint64_t dims[3] = {row_bytes, (cuuint64_t)a.d_out, (cuuint64_t)a.experts}, strides[2] = {row_bytes, row_bytes * a.d_out};
-    const cuuint32_t box[3] = {128, kTcRows, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.codes, dims, strides, box);
-}
 // x in boxes of 64 values of `rows` rows; with slots, it has been gathered into a row for each row of y.
 cudaError_t encode_x(CUtensorMap* map, const BaseArgs& a, int rows) {
     const cuuint64_t dims[2] = {(cuuint64_t)a.d_in, (cuuint64_t)(a.slot_of ? a.rows : a.x_rows)}, strides[1] = {(cuuint64_t)a.ldx * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)rows};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, dims, strides, box);
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, dims, strides, box);
 }
 
 template <int G, int NTOK, bool Z>

@@ -9,10 +9,21 @@ P = 1 << 20   # an aligned address that is never touched
 
 
 def product(**kw):
-    a = dict(x=P, ldx=256, T=2, d_in=256, d_out=8, codes=P, scales=P, sdt=0, zeros=None, group=64, y=P, ldy=8, ydt=0)
+    a = dict(x=P, ldx=256, T=2, d_in=256, d_out=8, codes=P, scales=P, sdt=0, zeros=None, group=64, y=P, ldy=8, ydt=0, ws=P, nws=1 << 30)
     a.update(kw)
     return sg.load_library().sgmv_base_product(a["x"], a["ldx"], a["T"], a["d_in"], a["d_out"], a["codes"], a["scales"], a["sdt"],
-                                               a["zeros"], a["group"], a["y"], a["ldy"], a["ydt"], None)
+                                               a["zeros"], a["group"], a["y"], a["ldy"], a["ydt"], a["ws"], a["nws"], None)
+
+
+def test_base_product_workspace():
+    lib = sg.load_library()
+    # 16-byte multiples of: 3 planes of digits, two int32 a group and an exponent for each row
+    assert lib.sgmv_base_product_workspace(1, 32, 32) == 96 + 16 + 16
+    assert lib.sgmv_base_product_workspace(3, 8192, 128) == 3 * 3 * 8192 + 3 * 64 * 8 + 16
+    assert lib.sgmv_base_product_workspace(0, 64, 64) == 0 and lib.sgmv_base_product_workspace(17, 8192, 128) == 0
+    for bad in ((-1, 64, 64), (1, 0, 64), (1, 64, 128), (1, 96, 64), (1, 1 << 21, 64), (1 << 24, 64, 64)):
+        assert lib.sgmv_base_product_workspace(*bad) == -1
+    assert product(ws=None) == 1 and product(ws=P + 8) == 1 and product(nws=10) == 8 and product(T=1 << 24) == 2
 
 
 @pytest.mark.parametrize("kw,why", [
@@ -38,9 +49,10 @@ def experts(**kw):
 
 def test_base_product_experts_workspace():
     lib = sg.load_library()
-    assert lib.sgmv_base_product_experts_workspace(16, 64, 1) == 0 and lib.sgmv_base_product_experts_workspace(0, 64, 3) == 0
-    assert lib.sgmv_base_product_experts_workspace(17, 64, 1) == 17 * 128
-    assert lib.sgmv_base_product_experts_workspace(-1, 64, 1) == lib.sgmv_base_product_experts_workspace(1, 64, 4097) == -1
+    f = lib.sgmv_base_product_experts_workspace
+    assert f(16, 64, 64, 1, 0) == f(16, 64, 64, 1, 1) == lib.sgmv_base_product_workspace(16, 64, 64) and f(0, 64, 64, 3, 1) == 0
+    assert f(17, 64, 64, 1, 0) == 0 and f(17, 64, 64, 1, 1) == 17 * 128
+    assert f(-1, 64, 64, 1, 0) == f(1, 64, 64, 4097, 0) == f(1, 64, 64, 0, 0) == f(1, 64, 16, 1, 0) == -1
     many = dict(rows=400, x_rows=400, slot_of=P)
     assert experts(**many) == 1 and b"workspace" in lib.sgmv_last_error()
     assert experts(**many, ws=P + 8, nws=1 << 20) == 1 and experts(**many, ws=P, nws=400 * 128 - 1) == 8
