@@ -616,9 +616,10 @@ SGMV_API sgmv_status sgmv_lora_delta_noalloc(const void* x, int64_t ldx, int32_t
  *          two calls that may overlap need two
  * T is 0..2^23 and d_out >= 1 any.  Sums are held in fp32 or exact integers, the
  * scale is applied in fp32 per group and the result rounded once.  From 17 rows on
- * the products (codes less zero points, times x) are exact.  Below, a row of x is
- * held in fixed point of 2^-22 of its largest value's binade, so that values down
- * to 2^-14 of the largest are exact and smaller ones off by at most 2^-23 of it.
+ * the products (codes less zero points, times x) are exact.  Below, each 256 values
+ * of a row of x are held in fixed point with a unit of 2^-21 of their largest one's
+ * binade: values down to 2^-14 of the largest are exact, smaller ones off by at
+ * most half a unit.
  * The order of the sum is fixed for given sizes: a call repeats bit for bit.  The
  * pointers belong to the current device.
  */

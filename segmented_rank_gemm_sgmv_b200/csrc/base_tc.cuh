@@ -14,6 +14,30 @@ constexpr int kTcRows = 128;           // rows of W in a tile
 constexpr int kStageK = 128;           // K values of an operand stage
 constexpr int kCodesK = 256;           // K values of a stage of codes: 128 bytes of a row
 
+// mbar_try_wait that lets the hardware suspend the thread for up to 0.1 ms: many warps wait here at a time, and their
+// polling would take the issue slots of those that work.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+        : "memory");
+    return ok != 0;
+}
+// Wait for a phase; gives up after kWaitLimitCycles, or when another thread of the block has (*abort_flag).
+__device__ __forceinline__ void wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+    if (mbar_try_wait_long(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!mbar_try_wait_long(bar, parity) && !*abort_flag)
+        if (clock64() - t0 > kWaitLimitCycles) {
+            atomicOr(err, kErrTimeout);
+            *abort_flag = 1;
+        }
+}
+
 __device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* map, int x, int y, int z, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(

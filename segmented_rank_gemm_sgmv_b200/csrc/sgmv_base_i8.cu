@@ -12,20 +12,21 @@ namespace {
 // y^T = W x^T in tiles of 128 rows of W and up to TT rows of x.
 //
 // With few rows of x the stream of codes should be the bound, and what stands in its way is turning codes into
-// tensor-core operands: to bf16, eight codes take 13 operations.  To bytes they take 3.  So a first kernel writes each
-// row of x in fixed point, X = x 2^(21 - E) rounded to an integer, |X| <= 2^22, E the exponent of the row's largest
-// value, as three signed digits of base 256, and tcgen05.mma (kind i8) multiplies the codes, 0..15, by the digits: a
+// tensor-core operands: to bf16, eight codes take 13 operations.  To bytes they take 3.  So a first kernel writes x in
+// fixed point: of each 256 values of a row, X = x 2^(21 - E) rounded to an integer, |X| <= 2^22, E the exponent of the
+// largest, as three signed digits of base 256.  tcgen05.mma (kind i8) multiplies the codes, 0..15, by the digits: a
 // group's sums are exact integers.  The epilogue takes z times the digits' sums from them, still exactly, joins the
-// digits in fp32 (hi = 256 a_2 + a_1 in 27 bits, then 256 hi + a_0 rounded once) and adds them, times the row's fp32
-// scale, to the total, which is multiplied by 2^(E - 21) at the end.
+// digits in fp32 (hi = 256 a_2 + a_1 in 27 bits, then 256 hi + a_0 rounded once) and adds them, times 2^(E - 21) and the
+// row's fp32 scale, to the total.
 //
-// The one rounding of x: values down to 2^-14 of the row's largest are exact (bf16 has 8 bits), smaller ones are off by
-// at most half a unit, 2^-23 of it, which is what an fp32 sum that holds the largest value rounds to.  A row that holds
-// an infinity or a NaN has no E: its outputs are summed in fp32 from the codes themselves, as the formula says.
+// The one rounding of x: values down to 2^-14 of the largest of their 256 are exact (bf16 has 8 bits), smaller ones are
+// off by at most half a unit, 2^-22 of its binade, which is what an fp32 sum that holds the largest value rounds to.
+// Values that are not finite have no E: their row's outputs, NaN so far, are summed in fp32 from the codes themselves.
 //
 // The digits' K order inside eight values is 0 2 4 6 1 3 5 7: the even and the odd nibbles of a word of codes are two
-// words of bytes.  The codes go to tensor memory as the A operand (a thread a row, a lane a row), three planes of
-// digits are the B operand: columns d TT + t.  Two lanes (MMA warp, accumulator, epilogue warps) take alternate groups.
+// words of bytes.  The codes go to tensor memory as the A operand (a thread a row, a lane a row); digit d of row t is
+// row 4 t + d of B, so that a row's sums are four neighbouring columns (the last one unused).  Two lanes (MMA warp,
+// accumulators, epilogue warps) take alternate groups, or pairs of groups where there is room for four accumulators.
 // K is split over the CTAs of a cluster; two CTAs share an SM.
 //
 // Roles: warp 0 streams codes (TMA), 2 copies digits (TMA), 1 and 3 issue the MMAs, 8 warps convert (half of them each
@@ -34,88 +35,74 @@ template <int TT>
 struct I8Config {
     static constexpr int kConvert = 8, kEpilogue = 8;                // warps
     static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
-    static constexpr int kCols = TT == 8 ? 32 : 48;                  // columns of an MMA: 3 TT, a multiple of 16
-    static constexpr int kStages = TT == 8 ? 6 : 5;                  // of 128 K values
+    static constexpr int kCols = 4 * TT;                             // columns of an MMA
+    static constexpr int kBatch = TT == 8 ? 2 : 1;                   // groups that a lane hands over together
+    static constexpr int kStages = 4;                                // of 128 K values
     static constexpr int kCodeStages = 3;                            // of 256 K values
-    static constexpr int kB = kCols * 128, kBCopied = 3 * TT * 128, kCodes = 128 * 128;
-    static constexpr int kTmemA = 2 * kCols, kTmem = 256;            // columns
+    static constexpr int kB = kCols * 128, kCodes = 128 * 128;
+    static constexpr int kTmemA = 2 * kBatch * kCols, kTmem = 256;   // columns
     static constexpr int kRedStride = 132;                           // floats of a row of totals
     static constexpr int kSmem = 1024 + kStages * kB + kCodeStages * kCodes;
     static_assert(kTmemA + kStages * 32 <= kTmem, "the stages fit");
     static_assert(2 * TT * kRedStride * 4 <= kCodeStages * kCodes, "the totals fit into the codes' memory");
 };
-constexpr int kNotFinite = 0x7fffffff;                               // in place of an exponent
 
 // What the first kernel writes, in the workspace.
 struct Digits {
-    int8_t* digits;            // [3][rows][d_in]
-    int2* sums;                // [groups][rows]: 256 S_2 + S_1 and S_0, the sums of a group's digits
-    int32_t* exponent;         // [rows]: E - 21, or kNotFinite
+    int8_t* digits;            // [rows][3][d_in]
+    int4* sums;                // [groups][rows]: 256 S_2 + S_1 and S_0, the sums of a group's digits, and 2^(E - 21) as fp32 bits
 };
 
-// 3-plane digits of each row of y's x.  A block a row: its largest magnitude, then its digits, 8 values a thread.
-__global__ void __launch_bounds__(1024) base_digits_kernel(BaseArgs a, Digits o, int group) {
+// A warp takes 256 values of a row, 8 a lane.
+__global__ void __launch_bounds__(256) base_digits_kernel(BaseArgs a, Digits o, int group, int blocks_per_row) {
     pdl_launch_dependents();
-    const int r = blockIdx.x, units = a.d_in / 8;
+    const int r = blockIdx.x / blocks_per_row, lane = threadIdx.x % 32;
+    const int u = blockIdx.x % blocks_per_row * 256 + threadIdx.x;   // unit of 8 values
     int xr = r;
     if (a.offsets && r >= a.offsets[a.experts]) return;              // a row of no expert
     if (a.slot_of) {
         const int slot = a.slot_of[r];
         xr = slot / a.k;
         if (slot < 0 || xr >= a.x_rows) {
-            if (threadIdx.x == 0) atomicOr(&g_err_base_i8, kErrRows);
+            if (u == 0) atomicOr(&g_err_base_i8, kErrRows);
             return;
         }
     }
-    const uint4* x = reinterpret_cast<const uint4*>(a.x + (int64_t)xr * a.ldx);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const bool in = u < a.d_in / 8;
+    if (in) v = reinterpret_cast<const uint4*>(a.x + (int64_t)xr * a.ldx)[u];
     // magnitudes of bf16 values compare as integers; an exponent of 255 is an infinity or a NaN
-    uint32_t most = 0;
-    for (int u = threadIdx.x; u < units; u += blockDim.x) {
-        const uint4 v = x[u];
-        most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-    }
-    most = max(most & 0xffffu, most >> 16);
-    most = __reduce_max_sync(0xffffffffu, most);
-    __shared__ uint32_t s_most[32];
-    if (threadIdx.x % 32 == 0) s_most[threadIdx.x / 32] = most;
-    __syncthreads();
-    most = threadIdx.x % 32 < blockDim.x / 32 ? s_most[threadIdx.x % 32] : 0;
-    most = __reduce_max_sync(0xffffffffu, most);
-    const bool finite = most < 0x7f80u;
-    // largest value < 2^(E + 1); below the normal range E = -126 serves, whose units are finer than the values'
+    uint32_t most = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+    // the largest is below 2^(E + 1); below the normal range E = -126 serves, whose units are finer than the values'
     const int e = max((int)(most >> 7), 1) - 127;
-    if (threadIdx.x == 0) o.exponent[r] = finite ? e - 21 : kNotFinite;
-    if (!finite) return;                 // the digits are not used
-    const int steps = (units + blockDim.x - 1) / blockDim.x;
-    for (int i = 0; i < steps; ++i) {
-        const int u = i * blockDim.x + threadIdx.x;
-        float f[8] = {};
-        if (u < units) unpack8(x[u], f);
-        uint32_t plane[3][2] = {};
-        int s1 = 0, s0 = 0, s2 = 0;
+    const float factor = most < 0x7f80u ? scalbnf(1.0f, e - 21) : __uint_as_float(0x7fc00000u);
+    float f[8];
+    unpack8(v, f);
+    uint32_t plane[3][2] = {};
+    int s2 = 0, s1 = 0, s0 = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int X = __float2int_rn(scalbnf(f[j], 21 - e));
-            const int d0 = (int8_t)X, X1 = (X - d0) >> 8, d1 = (int8_t)X1, d2 = (X1 - d1) >> 8;
-            const int at = j % 2, shift = j / 2 * 8;
-            plane[0][at] |= (uint32_t)(d0 & 0xff) << shift;
-            plane[1][at] |= (uint32_t)(d1 & 0xff) << shift;
-            plane[2][at] |= (uint32_t)(d2 & 0xff) << shift;
-            s0 += d0;
-            s1 += d1;
-            s2 += d2;
-        }
-        if (u < units)
-#pragma unroll
-            for (int d = 0; d < 3; ++d)
-                *reinterpret_cast<uint2*>(o.digits + ((int64_t)d * a.rows + r) * a.d_in + u * 8) = make_uint2(plane[d][0], plane[d][1]);
-        int hi = 256 * s2 + s1;
-        for (int k = 1; k < group / 8; k *= 2) {                     // a group's 4, 8 or 16 units are neighbouring lanes
-            hi += __shfl_xor_sync(0xffffffffu, hi, k);
-            s0 += __shfl_xor_sync(0xffffffffu, s0, k);
-        }
-        if (u < units && u % (group / 8) == 0) o.sums[(int64_t)(u / (group / 8)) * a.rows + r] = make_int2(hi, s0);
+    for (int j = 0; j < 8; ++j) {
+        const int X = __float2int_rn(scalbnf(f[j], 21 - e));         // any integer where values are not finite
+        const int d0 = (int8_t)X, X1 = (X - d0) >> 8, d1 = (int8_t)X1, d2 = (int8_t)((X1 - d1) >> 8);
+        const int at = j % 2, shift = j / 2 * 8;
+        plane[0][at] |= (uint32_t)(d0 & 0xff) << shift;
+        plane[1][at] |= (uint32_t)(d1 & 0xff) << shift;
+        plane[2][at] |= (uint32_t)(d2 & 0xff) << shift;
+        s0 += d0;
+        s1 += d1;
+        s2 += d2;
     }
+    if (in)
+#pragma unroll
+        for (int d = 0; d < 3; ++d)
+            *reinterpret_cast<uint2*>(o.digits + ((int64_t)r * 3 + d) * a.d_in + u * 8) = make_uint2(plane[d][0], plane[d][1]);
+    int hi = 256 * s2 + s1;
+    for (int k = 1; k < group / 8; k *= 2) {                         // a group's 4, 8 or 16 units are neighbouring lanes
+        hi += __shfl_xor_sync(0xffffffffu, hi, k);
+        s0 += __shfl_xor_sync(0xffffffffu, s0, k);
+    }
+    if (in && lane % (group / 8) == 0) o.sums[(int64_t)(u / (group / 8)) * a.rows + r] = make_int4(hi, s0, __float_as_int(factor), 0);
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T on bytes, A unsigned and B signed, to int32: A has a lane a row and four consecutive
@@ -142,7 +129,7 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
         s_afull[2], s_aempty[2], s_done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ int2 s_sums[C::kEpilogue][TT];
+    __shared__ int4 s_sums[C::kEpilogue][C::kBatch][TT];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
     const int rank = blockIdx.x % n_split, n0 = (int)(blockIdx.x / n_split) * kTcRows;
     uint8_t* stages = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;  // [kStages][kCols] rows of 128 digits
@@ -158,7 +145,7 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
     const int c0 = (int)((int64_t)all * rank / n_split), c1 = (int)((int64_t)all * (rank + 1) / n_split);
     const int k_begin = c0 * kCodesK, k_end = min(a.d_in, c1 * kCodesK), n_k = (k_end - k_begin + kStageK - 1) / kStageK;
     const int groups = a.d_in / G;
-    constexpr bool kAlone = G == kStageK;                            // each stage is one lane's
+    constexpr bool kAlone = G * C::kBatch >= kStageK;                // each stage is one lane's
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -187,15 +174,7 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     // waits give up together: whoever runs out of time stops the others' waits too
     volatile int* abort_flag = &s_abort;
-    const auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity)) return;
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar, parity) && !*abort_flag)
-            if (clock64() - t0 > kWaitLimitCycles) {
-                atomicOr(&g_err_base_i8, kErrTimeout);
-                *abort_flag = 1;
-            }
-    };
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { wait_or_abort(bar, parity, abort_flag, &g_err_base_i8); };
     float* red = reinterpret_cast<float*>(codes);                    // [2 TT][kRedStride] totals
 
     // registers at launch: 5 warpgroups of 48 = 40 + 2 x 40 + 2 x 56 and some
@@ -222,10 +201,8 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
                     const int s = kt % C::kStages;
                     if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
                     if (*abort_flag) break;
-                    mbar_arrive_expect_tx(&s_full[s], C::kBCopied);
-#pragma unroll
-                    for (int d = 0; d < 3; ++d)
-                        tma_load_3d(stages + s * C::kB + d * TT * 128, &digits_map, k_begin + kt * kStageK, row0, d, &s_full[s]);
+                    mbar_arrive_expect_tx(&s_full[s], C::kB);
+                    tma_load_3d(stages + s * C::kB, &digits_map, k_begin + kt * kStageK, 0, row0, &s_full[s]);
                 }
                 if (*abort_flag)         // no copy is left in flight
                     for (int j = max(0, kt - C::kStages); j < kt; ++j) mbar_wait(&s_full[j % C::kStages], (j / C::kStages) & 1, &g_err_base_i8);
@@ -233,36 +210,40 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
         } else {
             const int ln = warp / 2;     // 0 or 1
             const uint64_t bdesc = smem_desc_sw128(smem_u32(stages), 16, 1024);
-            const uint32_t d = tmem + ln * C::kCols;
+            const uint32_t d = tmem + ln * (C::kBatch * C::kCols);
             constexpr uint32_t idesc = idesc_u8_s8(128, C::kCols);
-            int n = 0, g = 0;            // this lane's groups begun; the stage's first group
-            for (int kt = kAlone ? ln : 0; kt < n_k; kt += kAlone ? 2 : 1) {
+            const int all_groups = (k_end - k_begin) / G;
+            int n = 0;                   // this lane's batches begun
+            for (int kt = 0; kt < n_k; ++kt) {
+                const int first = kt * (kStageK / G);
+                if (kAlone && first / C::kBatch % 2 != ln) continue;
                 const int s = kt % C::kStages;
                 wait(&s_full[s], (kt / C::kStages) & 1);
                 tc_fence_after();
-                const int n_groups = min(kStageK, k_end - k_begin - kt * kStageK) / G;
                 const uint32_t at = tmem + C::kTmemA + s * 32;
                 const uint64_t bd = bdesc + (uint64_t)(s * (C::kB / 16));
 #pragma unroll
                 for (int gi = 0; gi < kStageK / G; ++gi) {
-                    if (gi >= n_groups) break;
-                    if (!kAlone && (g + gi) % 2 != ln) continue;
-                    if (n > 0) {
-                        wait(&s_aempty[ln], (n - 1) & 1);
-                        tc_fence_after();
+                    const int g = first + gi, part = g % C::kBatch;
+                    if (g >= all_groups) break;
+                    if (!kAlone && g / C::kBatch % 2 != ln) continue;
+                    if (part == 0) {
+                        if (n > 0) {
+                            wait(&s_aempty[ln], (n - 1) & 1);
+                            tc_fence_after();
+                        }
+                        ++n;
                     }
-                    ++n;
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < G / 32; ++i) {
                             const int ks = gi * (G / 32) + i;
-                            tc_mma_i8_ts(d, at + ks * 8, bd + ks * 2, idesc, i > 0);
+                            tc_mma_i8_ts(d + part * C::kCols, at + ks * 8, bd + ks * 2, idesc, i > 0);
                         }
-                        tc_commit(&s_afull[ln]);
+                        if (part == C::kBatch - 1 || g == all_groups - 1) tc_commit(&s_afull[ln]);
                     }
                     __syncwarp();
                 }
-                g += n_groups;
                 if (elect_one()) tc_commit(&s_empty[s]);     // arrives at once where this lane had no group
                 __syncwarp();
             }
@@ -314,10 +295,12 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
         load_scales(next, a.scales, srow + g0, groups - g0, scale_f32, vec);
         if constexpr (Z) z_next = load_zeros<kGroups>(a.zeros, srow + g0, groups - g0, vec);
         const auto sums_of = [&](int g) {                            // lane t: row t's sums of group g
-            return g < g1 && lane < n_tok ? in.sums[(int64_t)g * a.rows + row0 + lane] : make_int2(0, 0);
+            return g < g1 && lane < n_tok ? in.sums[(int64_t)g * a.rows + row0 + lane] : make_int4(0, 0, 0, 0);
         };
-        int2 sums = sums_of(g0 + ln);
-        int n = 0;                       // groups done
+        int4 sums[C::kBatch];            // of the lane's next batch
+#pragma unroll
+        for (int i = 0; i < C::kBatch; ++i) sums[i] = sums_of(g0 + ln * C::kBatch + i);
+        int n = 0;                       // batches done
         for (int gs = g0; gs < g1; gs += kGroups) {
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) now[i] = next[i];
@@ -328,34 +311,39 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
             }
 #pragma unroll
             for (int gi = 0; gi < kGroups; ++gi) {
+                const int g = gs - g0 + gi, part = gi % C::kBatch;   // a span begins with a batch
                 if (gs + gi >= g1) break;
-                if (gi % 2 != ln) continue;                          // a span begins at an even group
+                if (g / C::kBatch % 2 != ln) continue;
                 const float sc = scale_of(now, gi, scale_f32);
                 const int z = Z ? (int)(z_now >> (8 * gi) & 0xffu) : 8;
-                if (lane < TT) s_sums[ew][lane] = sums;
-                __syncwarp();
-                sums = sums_of(gs + gi + 2);
-                wait(&s_afull[ln], n++ & 1);
-                tc_fence_after();
-                const uint32_t from = tmem + ln * C::kCols + ((uint32_t)(warp % 4 * 32) << 16);
+                if (part == 0) {
 #pragma unroll
-                for (int t = 0; t < TT; t += 8) {
+                    for (int i = 0; i < C::kBatch; ++i) {
+                        if (lane < TT) s_sums[ew][i][lane] = sums[i];
+                        sums[i] = sums_of(gs + gi + 2 * C::kBatch + i);
+                    }
+                    __syncwarp();
+                    wait(&s_afull[ln], n++ & 1);
+                    tc_fence_after();
+                }
+                const uint32_t from = tmem + (ln * C::kBatch + part) * C::kCols + ((uint32_t)(warp % 4 * 32) << 16);
+#pragma unroll
+                for (int t = 0; t < TT; t += 2) {
                     if (t >= n_tok) break;
-                    uint32_t d0[8], d1[8], d2[8];
-                    tmem_ld_x8(from + t, d0);
-                    tmem_ld_x8(from + TT + t, d1);
-                    tmem_ld_x8(from + 2 * TT + t, d2);
+                    uint32_t d[8];
+                    tmem_ld_x8(from + 4 * t, d);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int2 s = s_sums[ew][t + i];
-                        const int hi = (int)d2[i] * 256 + (int)d1[i] - z * s.x, lo = (int)d0[i] - z * s.y;
-                        total[t + i] = fmaf(sc, fmaf((float)hi, 256.0f, (float)lo), total[t + i]);
+                    for (int i = 0; i < 2; ++i) {
+                        const int4 s = s_sums[ew][part][t + i];
+                        const int hi = (int)d[4 * i + 2] * 256 + (int)d[4 * i + 1] - z * s.x, lo = (int)d[4 * i] - z * s.y;
+                        total[t + i] = fmaf(sc, fmaf((float)hi, 256.0f, (float)lo) * __int_as_float(s.z), total[t + i]);
                     }
                 }
-                tc_fence_before();
+                const bool done = part == C::kBatch - 1 || gs + gi == g1 - 1;
+                if (done) tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s_aempty[ln]);
+                if (done && lane == 0) mbar_arrive(&s_aempty[ln]);
             }
         }
         named_bar_sync(1, C::kEpilogue * 32);        // every code has been read: the totals take the codes' memory
@@ -370,12 +358,19 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
     const uint32_t base = smem_u32(red);
     for (int i = rank * C::kThreads + tid; i < n_tok * 128; i += n_split * C::kThreads) {
         const int t = i / 128, n = i % 128, row = row0 + t;
-        float v = 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < n_split; ++c) {
-            const uint32_t from = n_split > 1 ? map_cluster(base, c) : base;
-            v += ld_cluster_f32(from + (t * C::kRedStride + n) * 4) + ld_cluster_f32(from + ((TT + t) * C::kRedStride + n) * 4);
+        const uint32_t at0 = (t * C::kRedStride + n) * 4, at1 = at0 + TT * C::kRedStride * 4;
+        float u[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {    // all loads in flight before the sum
+            u[c] = 0.0f;
+            if (c < n_split) {
+                const uint32_t from = n_split > 1 ? map_cluster(base, c) : base;
+                u[c] = ld_cluster_f32(from + at0) + ld_cluster_f32(from + at1);
+            }
         }
+        float v = u[0];
+#pragma unroll
+        for (int c = 1; c < 8; ++c) v += u[c];
         if (n0 + n >= a.d_out || *abort_flag) continue;
         int xr = row;
         if (a.slot_of) {
@@ -383,10 +378,7 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
             xr = slot / a.k;
             if (slot < 0 || xr >= a.x_rows) continue;                // reported by the first kernel
         }
-        const int exponent = in.exponent[row];
-        if (exponent != kNotFinite) {
-            v = scalbnf(v, exponent);
-        } else {                         // infinities and NaN go their way through the formula
+        if (isnan(v)) {                  // infinities and NaN go their way through the formula
             const int64_t w = (int64_t)e * a.d_out + n0 + n;
             const uint16_t* x = a.x + (int64_t)xr * a.ldx;
             v = 0.0f;
@@ -426,8 +418,9 @@ cudaError_t launch_t(const BaseArgs& a, const Digits& in, bool scale_f32, bool y
     if (err != cudaSuccess) return err;
     CUtensorMap map, digits_map;
     if ((err = encode_codes(&map, a)) != cudaSuccess) return err;
-    const cuuint64_t dims[3] = {(cuuint64_t)a.d_in, (cuuint64_t)a.rows, 3}, strides[2] = {(cuuint64_t)a.d_in, (cuuint64_t)a.rows * a.d_in};
-    const cuuint32_t box[3] = {kStageK, TT, 1};
+    // a fourth digit reads as 0
+    const cuuint64_t dims[3] = {(cuuint64_t)a.d_in, 3, (cuuint64_t)a.rows}, strides[2] = {(cuuint64_t)a.d_in, 3 * (cuuint64_t)a.d_in};
+    const cuuint32_t box[3] = {kStageK, 4, TT};
     if ((err = encode_map(&digits_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, in.digits, dims, strides, box)) != cudaSuccess) return err;
     const int tiles = (a.d_out + kTcRows - 1) / kTcRows, k_stages = (a.d_in + kCodesK - 1) / kCodesK;
     const int64_t units = a.offsets ? (int64_t)a.rows / TT + std::min(a.rows, a.experts) : ((int64_t)a.rows + TT - 1) / TT;
@@ -466,16 +459,15 @@ cudaError_t launch_g(const BaseArgs& a, int64_t per, const Digits& in, bool scal
 }  // namespace
 
 int64_t base_i8_workspace(int64_t rows, int64_t d_in, int64_t group) {
-    return round16(3 * rows * d_in) + round16(rows * (d_in / group) * 8) + round16(rows * 4);
+    return round16(3 * rows * d_in) + rows * (d_in / group) * 16;
 }
 
 cudaError_t launch_base_i8(const BaseArgs& a, int64_t per, bool scale_f32, bool y_f32, void* workspace, cudaStream_t stream) {
     uint8_t* w = static_cast<uint8_t*>(workspace);
     const int64_t rows = a.rows;
-    const Digits in{reinterpret_cast<int8_t*>(w), reinterpret_cast<int2*>(w + round16(3 * rows * a.d_in)),
-                    reinterpret_cast<int32_t*>(w + round16(3 * rows * a.d_in) + round16(rows * (a.d_in / a.group) * 8))};
-    const int threads = std::min(1024, std::max(32, (a.d_in / 8 + 31) / 32 * 32));
-    base_digits_kernel<<<(unsigned)a.rows, threads, 0, stream>>>(a, in, a.group);
+    const Digits in{reinterpret_cast<int8_t*>(w), reinterpret_cast<int4*>(w + round16(3 * rows * a.d_in))};
+    const int blocks_per_row = (a.d_in + 2047) / 2048;
+    base_digits_kernel<<<(unsigned)(a.rows * blocks_per_row), 256, 0, stream>>>(a, in, a.group, blocks_per_row);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     if (a.zeros)
         return a.group == 128  ? launch_g<128, true>(a, per, in, scale_f32, y_f32, stream)

@@ -136,15 +136,7 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     // waits give up together: whoever runs out of time stops the others' waits too
     volatile int* abort_flag = &s_abort;
-    const auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity)) return;
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar, parity) && !*abort_flag)
-            if (clock64() - t0 > kWaitLimitCycles) {
-                atomicOr(&g_err_base_tc, kErrTimeout);
-                *abort_flag = 1;
-            }
-    };
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { wait_or_abort(bar, parity, abort_flag, &g_err_base_tc); };
 
     float* red = reinterpret_cast<float*>(stages);                   // [2 kPassCols][kRedStride] totals
 

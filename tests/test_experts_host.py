@@ -17,9 +17,9 @@ def product(**kw):
 
 def test_base_product_workspace():
     lib = sg.load_library()
-    # 16-byte multiples of: 3 planes of digits, two int32 a group and an exponent for each row
-    assert lib.sgmv_base_product_workspace(1, 32, 32) == 96 + 16 + 16
-    assert lib.sgmv_base_product_workspace(3, 8192, 128) == 3 * 3 * 8192 + 3 * 64 * 8 + 16
+    # three digits a value and 16 bytes a group for each row
+    assert lib.sgmv_base_product_workspace(1, 32, 32) == 96 + 16
+    assert lib.sgmv_base_product_workspace(3, 8192, 128) == 3 * 3 * 8192 + 3 * 64 * 16
     assert lib.sgmv_base_product_workspace(0, 64, 64) == 0 and lib.sgmv_base_product_workspace(17, 8192, 128) == 0
     for bad in ((-1, 64, 64), (1, 0, 64), (1, 64, 128), (1, 96, 64), (1, 1 << 21, 64), (1 << 24, 64, 64)):
         assert lib.sgmv_base_product_workspace(*bad) == -1
