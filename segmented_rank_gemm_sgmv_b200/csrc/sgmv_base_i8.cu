@@ -29,11 +29,10 @@ namespace {
 // accumulators, epilogue warps) take alternate groups, or pairs of groups where there is room for four accumulators.
 // K is split over the CTAs of a cluster; two CTAs share an SM.
 //
-// Roles: warp 0 streams codes (TMA), 2 copies digits (TMA), 1 and 3 issue the MMAs, 8 warps convert (half of them each
-// stage), 8 are the epilogue.
+// Roles: warp 0 streams codes (TMA), 2 copies digits (TMA), 1 and 3 issue the MMAs, 4 warps convert, 8 are the epilogue.
 template <int TT>
 struct I8Config {
-    static constexpr int kConvert = 8, kEpilogue = 8;                // warps
+    static constexpr int kConvert = 4, kEpilogue = 8;                // warps
     static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
     static constexpr int kCols = 4 * TT;                             // columns of an MMA
     static constexpr int kBatch = TT == 8 ? 2 : 1;                   // groups that a lane hands over together
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
         }
         for (int i = 0; i < C::kCodeStages; ++i) {
             mbar_init(&s_cfull[i], 1);
-            mbar_init(&s_cempty[i], 256);
+            mbar_init(&s_cempty[i], 128);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_afull[i], 1);
@@ -177,7 +176,7 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
     const auto wait = [&](uint64_t* bar, uint32_t parity) { wait_or_abort(bar, parity, abort_flag, &g_err_base_i8); };
     float* red = reinterpret_cast<float*>(codes);                    // [2 TT][kRedStride] totals
 
-    // registers at launch: 5 warpgroups of 48 = 40 + 2 x 40 + 2 x 56 and some
+    // registers at launch: 4 warpgroups of 64 = 40 + 40 + 2 x 88
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
@@ -253,10 +252,10 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
         __syncwarp();
     } else if (warp < 4 + C::kConvert) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; of two sets of warps each takes alternate stages
+        const int r = tid - 128;         // a row
         const uint32_t to = tmem + C::kTmemA + ((uint32_t)(warp % 4 * 32) << 16);
         constexpr uint32_t kFlip = Z ? 0u : 0x08080808u;             // two's complement codes to excess 8
-        for (int kt = part; kt < n_k; kt += 2) {
+        for (int kt = 0; kt < n_k; ++kt) {
             const int s = kt % C::kStages, ci = kt / 2, cs = ci % C::kCodeStages;
             wait(&s_cfull[cs], (ci / C::kCodeStages) & 1);
             const uint8_t* cp = codes + cs * C::kCodes + r * 128;
@@ -279,10 +278,10 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&s_full[s]);
-            mbar_arrive(&s_cempty[cs]);
+            if (kt % 2 == 1) mbar_arrive(&s_cempty[cs]);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
         pdl_wait();
         const int ew = warp - 4 - C::kConvert, ln = ew / 4;
         const int erow = (warp % 4) * 32 + lane;
@@ -310,40 +309,46 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
                 if constexpr (Z) z_next = load_zeros<kGroups>(a.zeros, srow + gs + kGroups, groups - gs - kGroups, vec);
             }
 #pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi) {
-                const int g = gs - g0 + gi, part = gi % C::kBatch;   // a span begins with a batch
-                if (gs + gi >= g1) break;
-                if (g / C::kBatch % 2 != ln) continue;
-                const float sc = scale_of(now, gi, scale_f32);
-                const int z = Z ? (int)(z_now >> (8 * gi) & 0xffu) : 8;
-                if (part == 0) {
+            for (int b = 0; b < kGroups; b += C::kBatch) {           // a span begins with a batch
+                const int gb = gs + b;
+                if (gb >= g1) break;
+                if ((gb - g0) / C::kBatch % 2 != ln) continue;
+#pragma unroll
+                for (int i = 0; i < C::kBatch; ++i) {
+                    if (lane < TT) s_sums[ew][i][lane] = sums[i];
+                    sums[i] = sums_of(gb + 2 * C::kBatch + i);
+                }
+                __syncwarp();
+                wait(&s_afull[ln], n++ & 1);
+                tc_fence_after();
+                const uint32_t from = tmem + ln * (C::kBatch * C::kCols) + ((uint32_t)(warp % 4 * 32) << 16);
+#pragma unroll
+                for (int t = 0; t < TT; t += 4) {
+                    if (t >= n_tok) break;
+                    uint32_t d[C::kBatch][16];
+#pragma unroll
+                    for (int i = 0; i < C::kBatch; ++i) tmem_ld_x16(from + i * C::kCols + 4 * t, d[i]);
+                    tmem_ld_wait();
+                    if (t + 4 >= n_tok) {                            // all is in registers: the accumulators are free
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_aempty[ln]);
+                    }
 #pragma unroll
                     for (int i = 0; i < C::kBatch; ++i) {
-                        if (lane < TT) s_sums[ew][i][lane] = sums[i];
-                        sums[i] = sums_of(gs + gi + 2 * C::kBatch + i);
-                    }
-                    __syncwarp();
-                    wait(&s_afull[ln], n++ & 1);
-                    tc_fence_after();
-                }
-                const uint32_t from = tmem + (ln * C::kBatch + part) * C::kCols + ((uint32_t)(warp % 4 * 32) << 16);
+                        if (gb + i >= g1) break;
+                        const float sc = scale_of(now, b + i, scale_f32);
+                        const int z = Z ? (int)(z_now >> (8 * (b + i)) & 0xffu) : 8;
 #pragma unroll
-                for (int t = 0; t < TT; t += 2) {
-                    if (t >= n_tok) break;
-                    uint32_t d[8];
-                    tmem_ld_x8(from + 4 * t, d);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int4 s = s_sums[ew][part][t + i];
-                        const int hi = (int)d[4 * i + 2] * 256 + (int)d[4 * i + 1] - z * s.x, lo = (int)d[4 * i] - z * s.y;
-                        total[t + i] = fmaf(sc, fmaf((float)hi, 256.0f, (float)lo) * __int_as_float(s.z), total[t + i]);
+                        for (int j = 0; j < 4; ++j) {
+                            if (j % 2 == 0 && t + j >= n_tok) break;
+                            const int4 s = s_sums[ew][i][t + j];
+                            const int hi = (int)d[i][4 * j + 2] * 256 + (int)d[i][4 * j + 1] - z * s.x, lo = (int)d[i][4 * j] - z * s.y;
+                            total[t + j] = fmaf(sc, fmaf((float)hi, 256.0f, (float)lo) * __int_as_float(s.z), total[t + j]);
+                        }
                     }
                 }
-                const bool done = part == C::kBatch - 1 || gs + gi == g1 - 1;
-                if (done) tc_fence_before();
-                __syncwarp();
-                if (done && lane == 0) mbar_arrive(&s_aempty[ln]);
+                __syncwarp();            // every lane has read the sums
             }
         }
         named_bar_sync(1, C::kEpilogue * 32);        // every code has been read: the totals take the codes' memory
