@@ -209,33 +209,40 @@ __device__ __forceinline__ void store_vals(T* p, const float (&f)[V]) {
 }
 
 // y[t] = add[t] + sum_j w[t][j] ys[row_of[t][j]], summed in fp32 in the order of j and rounded once.
-// Without weights every w is 1 (the gather's gradient).  V = 8 where every row starts on 16 bytes and d is
-// a multiple of 8, else 1.
-template <typename TI, typename TO, int V>
+// Without weights every w is 1 (the gather's gradient).  A thread takes E units of V values, kRowThreads units apart: V = 8
+// where every row starts on 16 bytes and d is a multiple of 8, with E = 1; else V = 1, with E = 8, so that it has as
+// many bytes in flight.
+template <typename TI, typename TO, int V, int E>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const TI* ys, int64_t ldys, int32_t rows,
                                                               const int32_t* row_of, const float* w, int32_t k,
                                                               int32_t d, int32_t chunks, const TO* add, int64_t ldadd,
                                                               TO* y, int64_t ldy) {
     const int64_t t = blockIdx.x / chunks;
-    const int c = ((int)(blockIdx.x % chunks) * kRowThreads + threadIdx.x) * V;
-    if (c >= d) return;
-    float acc[V], f[V];
-    if (add) {
-        load_vals<TO, V>(add + t * ldadd + c, acc);
-    } else {
+    const int c0 = ((int)(blockIdx.x % chunks) * (E * kRowThreads) + threadIdx.x) * V;
+    if (c0 >= d) return;
+    float acc[E][V], f[E][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    for (int u = 0; u < E; ++u) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
+        if (add && c0 + u * kRowThreads * V < d) load_vals<TO, V>(add + t * ldadd + c0 + u * kRowThreads * V, acc[u]);
     }
-#pragma unroll 4
+#pragma unroll(E == 1 ? 4 : 2)
     for (int j = 0; j < k; ++j) {
         const int64_t r = load_row(row_of, t * k + j, rows);
         if (r < 0) continue;
         const float wj = w ? w[t * k + j] : 1.0f;
-        load_vals<TI, V>(ys + r * ldys + c, f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
+        for (int u = 0; u < E; ++u)
+            if (c0 + u * kRowThreads * V < d) load_vals<TI, V>(ys + r * ldys + c0 + u * kRowThreads * V, f[u]);
+#pragma unroll
+        for (int u = 0; u < E; ++u)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[u][i] = fmaf(wj, f[u][i], acc[u][i]);
     }
-    store_vals<TO, V>(y + t * ldy + c, acc);
+#pragma unroll
+    for (int u = 0; u < E; ++u)
+        if (c0 + u * kRowThreads * V < d) store_vals<TO, V>(y + t * ldy + c0 + u * kRowThreads * V, acc[u]);
 }
 
 // One slot (t, j) a block: dys[row] = w[t][j] dy[t], dw[t][j] = sum_c dy[t][c] ys[row][c].  Each thread sums
@@ -316,8 +323,8 @@ sgmv_status combine_typed(const char* who, const void* ys, int64_t ldys, int32_t
                      (!add || rows16(add, ldadd, sizeof(TO)));
     int32_t chunks;
     unsigned blocks;
-    if (sgmv_status st = grid_of(who, T, vec ? d / 8 : d, kRowThreads, &chunks, &blocks); st != SGMV_OK) return st;
-    auto kern = vec ? combine_kernel<TI, TO, 8> : combine_kernel<TI, TO, 1>;
+    if (sgmv_status st = grid_of(who, T, vec ? d / 8 : d, vec ? kRowThreads : 8 * kRowThreads, &chunks, &blocks); st != SGMV_OK) return st;
+    auto kern = vec ? combine_kernel<TI, TO, 8, 1> : combine_kernel<TI, TO, 1, 8>;
     kern<<<blocks, kRowThreads, 0, stream>>>(static_cast<const TI*>(ys), ldys, rows, row_of, w, k, d, chunks,
                                              static_cast<const TO*>(add), ldadd, static_cast<TO*>(y), ldy);
     SGMV_CUDA_TRY(cudaGetLastError());
