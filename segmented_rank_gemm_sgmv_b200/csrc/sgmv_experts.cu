@@ -154,21 +154,25 @@ __device__ __forceinline__ int load_row(const int32_t* row_of, int64_t i, int32_
 }
 
 // xs[row_of[t][j]] = x[t]: a block copies one chunk of one token's row to its k places, so x is read once.
-// U is the unit of the copy: 16 bytes where both sides allow it, else one element.
+// U is the unit of the copy: 16 bytes where both sides allow it, else one element; a thread takes E of them.
+template <typename U> __host__ __device__ constexpr int gather_units() { return sizeof(U) == 16 ? 2 : 8; }
 template <typename U>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(const U* x, int64_t ldx, int32_t units, int32_t chunks,
                                                              const int32_t* row_of, int32_t k, U* xs, int64_t ldxs,
                                                              int32_t rows) {
+    constexpr int E = gather_units<U>();
     const int64_t t = blockIdx.x / chunks;
-    const int u0 = (int)(blockIdx.x % chunks) * (2 * kRowThreads) + threadIdx.x, u1 = u0 + kRowThreads;
-    U a{}, b{};
-    if (u0 < units) a = x[t * ldx + u0];
-    if (u1 < units) b = x[t * ldx + u1];
+    const int u0 = (int)(blockIdx.x % chunks) * (E * kRowThreads) + threadIdx.x;
+    U v[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        if (u0 + i * kRowThreads < units) v[i] = x[t * ldx + u0 + i * kRowThreads];
     for (int j = 0; j < k; ++j) {
         const int64_t r = load_row(row_of, t * k + j, rows);
         if (r < 0) continue;
-        if (u0 < units) xs[r * ldxs + u0] = a;
-        if (u1 < units) xs[r * ldxs + u1] = b;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (u0 + i * kRowThreads < units) xs[r * ldxs + u0 + i * kRowThreads] = v[i];
     }
 }
 
@@ -259,18 +263,26 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const TO*
         return;
     }
     const float wj = w ? w[slot] : 1.0f;
-    float sum = 0.0f, g[V], f[V];
-    for (int c = threadIdx.x * V; c < d; c += kRowThreads * V) {
-        load_vals<TO, V>(dy + t * lddy + c, g);
-        if (dw) {
-            load_vals<TI, V>(ys + r * ldys + c, f);
+    constexpr int E = V == 1 ? 8 : 1;    // units whose loads are in flight together
+    float sum = 0.0f, g[E][V], f[E][V];
+    for (int c0 = threadIdx.x * V; c0 < d; c0 += E * kRowThreads * V) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum = fmaf(g[i], f[i], sum);
+        for (int u = 0; u < E; ++u) {
+            const int c = c0 + u * kRowThreads * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[u][i] = f[u][i] = 0.0f;
+            if (c < d) load_vals<TO, V>(dy + t * lddy + c, g[u]);
+            if (c < d && dw) load_vals<TI, V>(ys + r * ldys + c, f[u]);
         }
-        if (dys) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) g[i] *= wj;
-            store_vals<TI, V>(dys + r * lddys + c, g);
+        for (int u = 0; u < E; ++u) {
+            const int c = c0 + u * kRowThreads * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                sum = fmaf(g[u][i], f[u][i], sum);
+                g[u][i] *= wj;
+            }
+            if (c < d && dys) store_vals<TI, V>(dys + r * lddys + c, g[u]);
         }
     }
     if (!dw) return;
@@ -367,7 +379,7 @@ sgmv_status gather_typed(const void* x, int64_t ldx, int32_t T, int32_t units, c
                          void* xs, int64_t ldxs, int32_t rows, cudaStream_t stream) {
     int32_t chunks;
     unsigned blocks;
-    if (sgmv_status st = grid_of("expert_gather", T, units, 2 * kRowThreads, &chunks, &blocks); st != SGMV_OK) return st;
+    if (sgmv_status st = grid_of("expert_gather", T, units, gather_units<U>() * kRowThreads, &chunks, &blocks); st != SGMV_OK) return st;
     gather_kernel<U><<<blocks, kRowThreads, 0, stream>>>(static_cast<const U*>(x), ldx, units, chunks, row_of, k,
                                                          static_cast<U*>(xs), ldxs, rows);
     SGMV_CUDA_TRY(cudaGetLastError());
