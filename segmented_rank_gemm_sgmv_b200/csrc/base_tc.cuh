@@ -1,5 +1,6 @@
 // What the two tensor-core kernels of the base products share.
 #pragma once
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -156,6 +157,24 @@ __device__ __forceinline__ bool find_unit(const BaseArgs& a, int most, unsigned 
     *row = s_found[1];
     *row_end = s_found[2];
     return s_found[0] >= 0;
+}
+
+// Allows `kern` its shared memory, once a kernel and device (the call takes about a microsecond), and refuses a build
+// whose registers a thread differ from `registers`: setmaxnreg waits for good where a block has fewer at launch than its
+// warpgroups ask for.
+template <typename Kernel>
+cudaError_t prepare_kernel(Kernel kern, int smem, int registers, std::atomic<uint64_t>* done) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return e;
+    if (attr.numRegs != registers) return cudaErrorInvalidConfiguration;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    done->fetch_or(bit, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 // A tensor map with the 128-byte swizzle; what lies past an end reads as 0.

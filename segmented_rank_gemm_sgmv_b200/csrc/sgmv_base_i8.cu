@@ -34,6 +34,7 @@ template <int TT>
 struct I8Config {
     static constexpr int kConvert = 4, kEpilogue = 8;                // warps
     static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
+    static constexpr int kRegisters = 64;                            // a thread at launch
     static constexpr int kCols = 4 * TT;                             // columns of an MMA
     static constexpr int kBatch = TT == 8 ? 2 : 1;                   // groups that a lane hands over together
     static constexpr int kStages = 4;                                // of 128 K values
@@ -419,7 +420,8 @@ template <int G, int TT, bool Z>
 cudaError_t launch_t(const BaseArgs& a, const Digits& in, bool scale_f32, bool y_f32, cudaStream_t stream) {
     using C = I8Config<TT>;
     auto kern = base_i8_kernel<G, TT, Z>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t err = prepare_kernel(kern, C::kSmem, C::kRegisters, &done);
     if (err != cudaSuccess) return err;
     CUtensorMap map, digits_map;
     if ((err = encode_codes(&map, a)) != cudaSuccess) return err;

@@ -32,6 +32,7 @@ struct TcConfig {
     static constexpr int kConvert = NTOK == 256 ? 4 : NTOK == 128 || G < 128 ? 8 : 16;       // warps
     static constexpr int kEpilogue = NTOK == 256 ? 16 : 8;
     static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
+    static constexpr int kRegisters = NTOK == 256 ? 80 : kConvert == 8 ? 96 : 72;     // a thread at launch
     static constexpr int kPassCols = NTOK < 128 ? NTOK : 128;        // columns of an accumulator
     static constexpr int kCols = kPassCols / (kEpilogue / 8);        // of them, an epilogue warp's
     static constexpr int kStages = NTOK <= 64 ? 6 : 3;               // of 128 K values
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
     const int k_begin = c0 * 256, k_end = min(a.d_in, c1 * 256), n_k = (k_end - k_begin + kStageK - 1) / kStageK;
     const int n_pad = (n_tok + 15) / 16 * 16;    // columns of the MMAs
     const bool halves = n_pad > C::kPassCols;    // the lanes take half of the rows each, else alternate groups
+    const int half = (n_pad / 2 + 15) / 16 * 16; // then the first lane's rows
     const bool alone = !halves && G == kStageK;  // then each stage is one lane's
     const int groups = a.d_in / G;
 
@@ -161,8 +163,8 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
             }
         } else if (warp == 1 || warp == 3) {
             const int ln = warp / 2;     // 0 or 1
-            const uint64_t bdesc = smem_desc_sw128(smem_u32(stages), 16, 1024) + (halves ? ln * (C::kPassCols * 128 / 16) : 0);
-            const uint32_t idesc = idesc_bf16_f32(128, halves ? (ln ? n_pad - C::kPassCols : C::kPassCols) : n_pad, false, false);
+            const uint64_t bdesc = smem_desc_sw128(smem_u32(stages), 16, 1024) + (halves ? ln * half * (128 / 16) : 0);
+            const uint32_t idesc = idesc_bf16_f32(128, halves ? (ln ? n_pad - half : half) : n_pad, false, false);
             const uint32_t d = tmem + ln * C::kPassCols;
             int n = 0, g = 0;            // this lane's groups begun; the stage's first group
             for (int kt = alone ? ln : 0; kt < n_k; kt += alone ? 2 : 1) {
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int ew = warp - 4 - C::kConvert, ln = ew / (C::kEpilogue / 2);
         const int erow = (warp % 4) * 32 + lane, ecol = ew % (C::kEpilogue / 2) / 4 * C::kCols;     // of the lane's accumulator
-        const int cols = (halves ? (ln ? n_pad - C::kPassCols : C::kPassCols) : n_pad) - ecol;      // of this warp's that are used
+        const int cols = (halves ? (ln ? n_pad - half : half) : n_pad) - ecol;      // of this warp's that are used
         float total[C::kCols];
         const int64_t srow = ((int64_t)e * a.d_out + min(n0 + erow, a.d_out - 1)) * groups;
 #pragma unroll
@@ -310,9 +312,10 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
     const uint32_t base = smem_u32(red);
     for (int i = rank * C::kThreads + tid; i < n_tok * 128; i += n_split * C::kThreads) {
         const int t = i / 128, n = i % 128;
+        const int at = halves && t >= half ? C::kPassCols + t - half : t;    // of the totals' rows
         float v;
         if (n_split == 1) {
-            v = red[t * C::kRedStride + n];
+            v = red[at * C::kRedStride + n];
             if (!halves) v += red[(C::kPassCols + t) * C::kRedStride + n];
         } else {
             float u[8], w[8];
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
                 u[c] = w[c] = 0.0f;
                 if (c < n_split) {
                     const uint32_t from = map_cluster(base, c);
-                    u[c] = ld_cluster_f32(from + (t * C::kRedStride + n) * 4);
+                    u[c] = ld_cluster_f32(from + (at * C::kRedStride + n) * 4);
                     if (!halves) w[c] = ld_cluster_f32(from + ((C::kPassCols + t) * C::kRedStride + n) * 4);
                 }
             }
@@ -356,7 +359,8 @@ template <int G, int NTOK, bool Z>
 cudaError_t launch_t(const BaseArgs& a, bool scale_f32, bool y_f32, cudaStream_t stream) {
     using C = TcConfig<G, NTOK>;
     auto kern = base_tc_kernel<G, NTOK, Z>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t err = prepare_kernel(kern, C::kSmem, C::kRegisters, &done);
     if (err != cudaSuccess) return err;
     CUtensorMap map, x_map;
     if ((err = encode_codes(&map, a)) != cudaSuccess || (err = encode_x(&x_map, a, NTOK)) != cudaSuccess) return err;
