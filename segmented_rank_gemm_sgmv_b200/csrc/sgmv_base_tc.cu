@@ -54,6 +54,18 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
         : "memory");
 }
 
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+// setmaxnreg to N registers a thread, more (inc) or fewer than now; by whole warpgroups.  At the end all go back to the
+// launch's count, lest the epilogue of the block is compiled for the least of them (its spills took 15 us): the warps
+// that had taken registers give them up before the block's barrier, the others take theirs after it, since before it
+// some might still be waiting for registers themselves.
+template <int N, bool inc>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (inc) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Eight codes (value i in bits 4i..4i+3) less the zero point, as eight bf16 in order.  bf16 128 + n has the bits
 // 0x4300 | n for n < 128, so inserting the code and subtracting 128 + z is exact.  `flip` is 0x08080808 for two's
 // complement codes (n ^ 8 is the value plus 8; then z is 8).
@@ -100,6 +112,17 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
     const bool alone = !halves && G == kStageK;  // then each stage is one lane's
     const int groups = a.d_in / G;
 
+    const auto copy_codes = [&](int i) {
+        mbar_arrive_expect_tx(&s_cfull[i % C::kCodeStages], C::kCodes);
+        tma_load_3d(codes + i % C::kCodeStages * C::kCodes, &codes_map, (c0 + i) * 128, n0, e, &s_cfull[i % C::kCodeStages]);
+    };
+    const auto copy_x = [&](int kt) {
+        const int s = kt % C::kStages;
+        mbar_arrive_expect_tx(&s_full[s], C::kB);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            tma_load_2d(stages + s * C::kB + i * NTOK * 128, &x_map, k_begin + kt * kStageK + i * 64, row0, &s_full[s]);
+    };
     if (tid < NTOK) {
         int r = -1;
         if (tid < n_tok) {
@@ -127,6 +150,8 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
         mbar_init(&s_done, 2);
         s_abort = 0;
         fence_mbar_init();
+        for (int i = 0; i < min(C::kCodeStages, c1 - c0); ++i) copy_codes(i);      // the first copies start here
+        for (int kt = 0; kt < min(C::kStages, n_k); ++kt) copy_x(kt);
     }
     if (warp == 1) {
         tmem_alloc(&s_tmem, C::kTmem);
@@ -142,7 +167,6 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
 
     float* red = reinterpret_cast<float*>(stages);                   // [2 kPassCols][kRedStride] totals
 
-    int n_x = 0;                         // stages of x asked for
     if (warp < 4) {
         // registers at launch: 7 warpgroups of 72 = 40 + 4 x 56 + 2 x 120; 5 of 96 = 48 + 2 x 56 + 2 x 160; 6 of 80 =
         // 40 + 56 + 4 x 96
@@ -150,13 +174,11 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
             if (elect_one()) {
-                int i = 0;
+                int i = min(C::kCodeStages, c1 - c0);
                 for (; i < c1 - c0; ++i) {
-                    const int s = i % C::kCodeStages;
-                    if (i >= C::kCodeStages) wait(&s_cempty[s], (i / C::kCodeStages - 1) & 1);
+                    wait(&s_cempty[i % C::kCodeStages], (i / C::kCodeStages - 1) & 1);
                     if (*abort_flag) break;
-                    mbar_arrive_expect_tx(&s_cfull[s], C::kCodes);
-                    tma_load_3d(codes + s * C::kCodes, &codes_map, (c0 + i) * 128, n0, e, &s_cfull[s]);
+                    copy_codes(i);
                 }
                 for (int j = max(0, i - C::kCodeStages); j < i; ++j)         // no copy is left in flight
                     mbar_wait(&s_cfull[j % C::kCodeStages], (j / C::kCodeStages) & 1, &g_err_base_tc);
@@ -201,20 +223,18 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
             mbar_wait(&s_done, 0, &g_err_base_tc);
         } else if (warp == 2) {
             const bool copier = elect_one();
-            for (int kt = 0; copier && kt < n_k; ++kt) {
-                const int s = kt % C::kStages;
-                if (kt >= C::kStages) wait(&s_empty[s], (kt / C::kStages - 1) & 1);
+            int n_x = min(C::kStages, n_k);          // stages asked for
+            for (; copier && n_x < n_k; ++n_x) {
+                wait(&s_empty[n_x % C::kStages], (n_x / C::kStages - 1) & 1);
                 if (*abort_flag) break;
-                uint8_t* bs = stages + s * C::kB;
-                mbar_arrive_expect_tx(&s_full[s], C::kB);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) tma_load_2d(bs + i * NTOK * 128, &x_map, k_begin + kt * kStageK + i * 64, row0, &s_full[s]);
-                n_x = kt + 1;
+                copy_x(n_x);
             }
             if (*abort_flag)             // no copy is left in flight
                 for (int kt = max(0, n_x - C::kStages); kt < n_x; ++kt) mbar_wait(&s_full[kt % C::kStages], (kt / C::kStages) & 1, &g_err_base_tc);
         }
         __syncwarp();
+        named_bar_sync(2, C::kThreads);
+        set_registers<C::kRegisters, true>();
     } else if (warp < 4 + C::kConvert) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int r = (tid - 128) % 128, part = (warp - 4) / 4;      // a row; of two sets of warps each takes alternate stages
@@ -257,6 +277,8 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
             mbar_arrive(&s_full[s]);
             if (kParts > 1 || kt % 2 == 1) mbar_arrive(&s_cempty[cs]);
         }
+        named_bar_sync(2, C::kThreads);
+        set_registers<C::kRegisters, true>();
     } else {
         if constexpr (NTOK == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         else if constexpr (C::kConvert == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
@@ -305,37 +327,50 @@ __global__ void __launch_bounds__(TcConfig<G, NTOK>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < C::kCols; ++i)
             if (i < cols) red[(ln * C::kPassCols + ecol + i) * C::kRedStride + erow] = total[i];
+        set_registers<C::kRegisters, false>();
+        named_bar_sync(2, C::kThreads);
     }
-    __syncthreads();                     // every copy and MMA is complete: each was waited for
     // the totals of the lanes and of the cluster's CTAs, in a fixed order
     if (n_split > 1) cluster_sync();
+    // (a warp a row: the registers straight to y, 64 bytes of a row at a time, took 4.5 us more for 256 rows)
     const uint32_t base = smem_u32(red);
-    for (int i = rank * C::kThreads + tid; i < n_tok * 128; i += n_split * C::kThreads) {
-        const int t = i / 128, n = i % 128;
+    const int n = n0 + lane * 4;
+    const bool dead = *abort_flag, wide = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (y_f32 ? 16 : 8) == 0 && n + 4 <= a.d_out;
+    for (int t = rank * (C::kThreads / 32) + warp; t < n_tok; t += n_split * (C::kThreads / 32)) {
         const int at = halves && t >= half ? C::kPassCols + t - half : t;    // of the totals' rows
-        float v;
+        const uint32_t at0 = (at * C::kRedStride + lane * 4) * 4, at1 = at0 + C::kPassCols * C::kRedStride * 4;
+        float4 v;
         if (n_split == 1) {
-            v = red[at * C::kRedStride + n];
-            if (!halves) v += red[(C::kPassCols + t) * C::kRedStride + n];
+            v = *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(red) + at0);
+            if (!halves) v = add4(v, *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(red) + at1));
         } else {
-            float u[8], w[8];
+            float4 u[8], w[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                u[c] = w[c] = 0.0f;
+                u[c] = w[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (c < n_split) {
                     const uint32_t from = map_cluster(base, c);
-                    u[c] = ld_cluster_f32(from + (at * C::kRedStride + n) * 4);
-                    if (!halves) w[c] = ld_cluster_f32(from + ((C::kPassCols + t) * C::kRedStride + n) * 4);
+                    u[c] = ld_cluster_v4(from + at0);
+                    if (!halves) w[c] = ld_cluster_v4(from + at1);
                 }
             }
-            v = u[0] + w[0];
+            v = add4(u[0], w[0]);
 #pragma unroll
-            for (int c = 1; c < 8; ++c) v += u[c] + w[c];
+            for (int c = 1; c < 8; ++c) v = add4(v, add4(u[c], w[c]));
         }
-        if (n0 + n < a.d_out && s_xrow[t] >= 0 && !*abort_flag) {
-            const int64_t to = (int64_t)(row0 + t) * a.ldy + n0 + n;
-            if (y_f32) static_cast<float*>(a.y)[to] = v;
-            else static_cast<uint16_t*>(a.y)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        if (s_xrow[t] < 0 || dead) continue;
+        const int64_t to = (int64_t)(row0 + t) * a.ldy + n;
+        if (wide) {
+            if (y_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.y) + to) = v;
+            else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + to) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            continue;
+        }
+        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (n + i >= a.d_out) break;
+            if (y_f32) static_cast<float*>(a.y)[to + i] = f[i];
+            else static_cast<uint16_t*>(a.y)[to + i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
         }
     }
     if (n_split > 1) {
