@@ -137,7 +137,10 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
 
     // the unit: up to TT consecutive rows of y of one matrix
     int e = 0, row0 = blockIdx.y * TT, row_end = min(a.rows, (int)(blockIdx.y + 1) * TT);
-    if (a.offsets && !find_unit<C::kThreads>(a, TT, &g_err_base_i8, &e, &row0, &row_end)) return;
+    if (a.offsets && !find_unit<C::kThreads>(a, TT, &g_err_base_i8, &e, &row0, &row_end)) {
+        pdl_wait();                      // nothing of this call ends before the first kernel does
+        return;
+    }
     const int n_tok = row_end - row0;
 
     // this CTA's code stages of K and operand stages
@@ -145,6 +148,11 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
     const int c0 = (int)((int64_t)all * rank / n_split), c1 = (int)((int64_t)all * (rank + 1) / n_split);
     const int k_begin = c0 * kCodesK, k_end = min(a.d_in, c1 * kCodesK), n_k = (k_end - k_begin + kStageK - 1) / kStageK;
     const int groups = a.d_in / G;
+    const auto copy_codes = [&](int i) {
+        const int s = i % C::kCodeStages;
+        mbar_arrive_expect_tx(&s_cfull[s], C::kCodes);
+        tma_load_3d(codes + s * C::kCodes, &codes_map, (c0 + i) * (kCodesK / 2), n0, e, &s_cfull[s]);
+    };
     constexpr bool kAlone = G * C::kBatch >= kStageK;                // each stage is one lane's
 
     if (tid == 0) {
@@ -163,6 +171,8 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
         mbar_init(&s_done, 2);
         s_abort = 0;
         fence_mbar_init();
+        // the codes are not the first kernel's: their copies start here and do not wait for it
+        for (int i = 0; i < min(C::kCodeStages, c1 - c0); ++i) copy_codes(i);
     }
     if (warp == 1) {
         tmem_alloc(&s_tmem, C::kTmem);
@@ -181,14 +191,12 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
-            if (elect_one()) {           // the codes are not the first kernel's: they need not wait for it
-                int i = 0;
+            if (elect_one()) {
+                int i = min(C::kCodeStages, c1 - c0);
                 for (; i < c1 - c0; ++i) {
-                    const int s = i % C::kCodeStages;
-                    if (i >= C::kCodeStages) wait(&s_cempty[s], (i / C::kCodeStages - 1) & 1);
+                    wait(&s_cempty[i % C::kCodeStages], (i / C::kCodeStages - 1) & 1);
                     if (*abort_flag) break;
-                    mbar_arrive_expect_tx(&s_cfull[s], C::kCodes);
-                    tma_load_3d(codes + s * C::kCodes, &codes_map, (c0 + i) * (kCodesK / 2), n0, e, &s_cfull[s]);
+                    copy_codes(i);
                 }
                 for (int j = max(0, i - C::kCodeStages); j < i; ++j)         // no copy is left in flight
                     mbar_wait(&s_cfull[j % C::kCodeStages], (j / C::kCodeStages) & 1, &g_err_base_i8);
@@ -358,7 +366,6 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
             if (i < n_tok) red[(ln * TT + i) * C::kRedStride + erow] = total[i];
     }
     __syncthreads();                     // every copy and MMA is complete: each was waited for
-    pdl_wait();
     // the totals of the lanes and of the cluster's CTAs, in a fixed order
     if (n_split > 1) cluster_sync();
     const uint32_t base = smem_u32(red);
