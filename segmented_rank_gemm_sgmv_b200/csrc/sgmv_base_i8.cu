@@ -30,13 +30,14 @@ namespace {
 // K is split over the CTAs of a cluster; two CTAs share an SM.
 //
 // Roles: warp 0 streams codes (TMA), 2 copies digits (TMA), 1 and 3 issue the MMAs, 4 warps convert, 8 are the epilogue.
-template <int TT>
+template <int G, int TT>
 struct I8Config {
     static constexpr int kConvert = 4, kEpilogue = 8;                // warps
     static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
     static constexpr int kRegisters = 64;                            // a thread at launch
     static constexpr int kCols = 4 * TT;                             // columns of an MMA
-    static constexpr int kBatch = TT == 8 ? 2 : 1;                   // groups that a lane hands over together
+    static constexpr int kBatch = TT == 4 && G < 128 ? 4 : TT <= 8 ? 2 : 1;      // groups that a lane hands over together
+    static constexpr int kLoad = kBatch < 2 ? kBatch : 2;            // of them, in registers at a time
     static constexpr int kStages = 4;                                // of 128 K values
     static constexpr int kCodeStages = 3;                            // of 256 K values
     static constexpr int kB = kCols * 128, kCodes = 128 * 128;
@@ -119,10 +120,10 @@ __device__ __forceinline__ void tc_mma_i8_ts(uint32_t d_tmem, uint32_t a_tmem, u
 __host__ __device__ constexpr uint32_t idesc_u8_s8(int M, int N) { return (2u << 4) | (0u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 
 template <int G, int TT, bool Z>
-__global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
+__global__ void __launch_bounds__(I8Config<G, TT>::kThreads, 2)
     base_i8_kernel(BaseArgs a, Digits in, const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap digits_map,
                    bool scale_f32, bool y_f32, bool vec, int n_split) {
-    using C = I8Config<TT>;
+    using C = I8Config<G, TT>;
     constexpr int kSpan = G == 32 ? 128 : 256, kGroups = kSpan / G;  // K values whose scales are loaded together
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages], s_cfull[C::kCodeStages], s_cempty[C::kCodeStages],
@@ -334,26 +335,29 @@ __global__ void __launch_bounds__(I8Config<TT>::kThreads, 2)
 #pragma unroll
                 for (int t = 0; t < TT; t += 4) {
                     if (t >= n_tok) break;
-                    uint32_t d[C::kBatch][16];
 #pragma unroll
-                    for (int i = 0; i < C::kBatch; ++i) tmem_ld_x16(from + i * C::kCols + 4 * t, d[i]);
-                    tmem_ld_wait();
-                    if (t + 4 >= n_tok) {                            // all is in registers: the accumulators are free
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s_aempty[ln]);
-                    }
+                    for (int i0 = 0; i0 < C::kBatch; i0 += C::kLoad) {
+                        uint32_t d[C::kLoad][16];
 #pragma unroll
-                    for (int i = 0; i < C::kBatch; ++i) {
-                        if (gb + i >= g1) break;
-                        const float sc = scale_of(now, b + i, scale_f32);
-                        const int z = Z ? (int)(z_now >> (8 * (b + i)) & 0xffu) : 8;
+                        for (int i = 0; i < C::kLoad; ++i) tmem_ld_x16(from + (i0 + i) * C::kCols + 4 * t, d[i]);
+                        tmem_ld_wait();
+                        if (t + 4 >= n_tok && i0 + C::kLoad == C::kBatch) {      // all is in registers: the accumulators are free
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s_aempty[ln]);
+                        }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (j % 2 == 0 && t + j >= n_tok) break;
-                            const int4 s = s_sums[ew][i][t + j];
-                            const int hi = (int)d[i][4 * j + 2] * 256 + (int)d[i][4 * j + 1] - z * s.x, lo = (int)d[i][4 * j] - z * s.y;
-                            total[t + j] = fmaf(sc, fmaf((float)hi, 256.0f, (float)lo) * __int_as_float(s.z), total[t + j]);
+                        for (int i = 0; i < C::kLoad; ++i) {
+                            if (gb + i0 + i >= g1) break;
+                            const float sc = scale_of(now, b + i0 + i, scale_f32);
+                            const int z = Z ? (int)(z_now >> (8 * (b + i0 + i)) & 0xffu) : 8;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if (j % 2 == 0 && t + j >= n_tok) break;
+                                const int4 s = s_sums[ew][i0 + i][t + j];
+                                const int hi = (int)d[i][4 * j + 2] * 256 + (int)d[i][4 * j + 1] - z * s.x, lo = (int)d[i][4 * j] - z * s.y;
+                                total[t + j] = fmaf(sc, fmaf((float)hi, 256.0f, (float)lo) * __int_as_float(s.z), total[t + j]);
+                            }
                         }
                     }
                 }
@@ -425,7 +429,7 @@ int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 
 template <int G, int TT, bool Z>
 cudaError_t launch_t(const BaseArgs& a, const Digits& in, bool scale_f32, bool y_f32, cudaStream_t stream) {
-    using C = I8Config<TT>;
+    using C = I8Config<G, TT>;
     auto kern = base_i8_kernel<G, TT, Z>;
     static std::atomic<uint64_t> done{0};
     cudaError_t err = prepare_kernel(kern, C::kSmem, C::kRegisters, &done);
@@ -467,6 +471,10 @@ cudaError_t launch_t(const BaseArgs& a, const Digits& in, bool scale_f32, bool y
 
 template <int G, bool Z>
 cudaError_t launch_g(const BaseArgs& a, int64_t per, const Digits& in, bool scale_f32, bool y_f32, cudaStream_t stream) {
+    // Four rows leave room for batches of four groups of 32 or 64 (28672 x 8192, groups of 64, one row: 43 us, with the
+    // eight-row kernel's two groups 46).  Experts of two rows on average and groups of 128, whose batches are two here
+    // too, only lose by units of four rows: 56.8 against 55.6 us for 64 experts of 1536 x 4096.
+    if (per <= 4 && (G < 128 || !a.offsets)) return launch_t<G, 4, Z>(a, in, scale_f32, y_f32, stream);
     return per <= 8 ? launch_t<G, 8, Z>(a, in, scale_f32, y_f32, stream) : launch_t<G, 16, Z>(a, in, scale_f32, y_f32, stream);
 }
 
