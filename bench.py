@@ -156,15 +156,19 @@ class ClockSampler:
                 "reasons": sorted(self.reasons), "samples": len(self.samples)}
 
 
+# The kernels of csrc/ that no delta call launches: base products and tokens sorted by expert.
+OTHER_OPERATORS = ("base_tc.cuh", "experts.h", "sgmv_base.cu", "sgmv_base_i8.cu", "sgmv_base_tc.cu", "sgmv_experts.cu")
+
+
 def source_digest() -> str:
-    """sha256 (first 16 hex digits) of the library's code: csrc/* by name, with `//`
+    """sha256 (first 16 hex digits) of the delta's code: csrc/* by name without OTHER_OPERATORS, with `//`
     comments, trailing blanks and empty lines removed, so that a comment edit keeps
     the counters while any code change drops them."""
     import hashlib
     import re
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "segmented_rank_gemm_sgmv_b200", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in sorted(set(os.listdir(csrc)) - set(OTHER_OPERATORS)):
         with open(os.path.join(csrc, name), encoding="utf-8", errors="replace") as f:
             for line in f:
                 code = re.sub(r"//.*", "", line).rstrip()
