@@ -686,7 +686,8 @@ SGMV_API sgmv_status sgmv_expert_order(const int32_t* expert_ids, int32_t T, int
  * as they were.  x and xs are device [T][ldx] and [rows][ldxs] of d values,
  * dtype 0 = bf16, 1 = fp32, aligned to their type (rows that all start on 16
  * bytes are copied faster).  row_of comes from sgmv_expert_order: no row twice.
- * A row outside 0..rows-1 other than -1 is skipped and reported.
+ * A row outside 0..rows-1 other than -1 is skipped and reported.  Here and below k is
+ * 1..64, T * k at most 2^30 and d at most 2^30.
  */
 SGMV_API sgmv_status sgmv_expert_gather(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t dtype,
                                         const int32_t* row_of, int32_t k, void* xs, int64_t ldxs, int32_t rows,

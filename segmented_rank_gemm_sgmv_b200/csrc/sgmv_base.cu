@@ -2,7 +2,6 @@
 // expert over rows sorted by expert.  Argument checks and the choice of the kernel.
 #include <algorithm>
 #include <string>
-#include <type_traits>
 
 #include "experts.h"
 #include "ptx.cuh"
@@ -15,7 +14,9 @@ namespace {
 
 // Rows of a matrix, on average.
 int64_t rows_each(int64_t rows, int64_t experts) { return (rows + experts - 1) / experts; }
-// From this many rows a matrix on, the bf16 kernel is the faster.
+// From this many rows a matrix on, the bf16 kernel is the faster: the integer kernel's epilogue grows with the rows and
+// with more of them a matrix it would read the codes again.  8192 x 8192, groups of 128: 16 rows 19.5 us by the integer
+// kernel, 24 rows 19.1 us by the bf16 kernel; one row 14.8 and 18.8 us.
 constexpr int kTcFrom = 17;
 
 int64_t workspace_bytes(int64_t rows, int64_t experts, int64_t d_in, int64_t group, bool slots) {

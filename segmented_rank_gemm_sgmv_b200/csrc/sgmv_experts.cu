@@ -13,8 +13,8 @@ __device__ unsigned int g_err_experts;
 
 namespace {
 
-constexpr int kOrderThreads = 512, kOrderWarps = kOrderThreads / 32;
-constexpr int kOrderTile = 2048;       // slots of a block when there are several
+constexpr int kOrderThreads = 512;     // of the counting kernel
+constexpr int kOrderTile = 512;        // slots of a block when there are several
 constexpr int kOrderMaxBlocks = 148;   // one wave of blocks
 constexpr int kOrderCounts = 65536;    // most block counts that the second kernel's blocks each read
 
@@ -26,8 +26,14 @@ int order_blocks(int64_t n, int experts) {
     return (int)std::min<int64_t>(most, (n + kOrderTile - 1) / kOrderTile);
 }
 
-// Warps of the ordering kernel: each keeps a count per expert in shared memory.
-int order_warps(int experts) { return experts <= 2048 ? kOrderWarps : kOrderWarps / 2; }
+// Warps of the ordering kernel, for a tile of slots: each step of a warp takes 32 of them, and its steps follow one
+// another; each warp keeps a count per expert in shared memory.
+int order_warps(int64_t tile, int experts) {
+    const int most = experts <= 1024 ? 32 : experts <= 2048 ? 16 : 8;
+    int warps = 4;
+    while (warps < most && warps * 32 < tile) warps *= 2;
+    return warps;
+}
 
 __device__ __forceinline__ int load_id(const int32_t* ids, int64_t i, int64_t end, int experts) {
     if (i >= end) return -1;
@@ -35,6 +41,18 @@ __device__ __forceinline__ int load_id(const int32_t* ids, int64_t i, int64_t en
     if (id >= 0 && id < experts) return id;
     if (id != -1) atomicOr(&g_err_experts, kErrExpert);
     return -1;
+}
+
+// The lanes whose id (-1 or below 2^bits) is this lane's; any mask where it is -1.  A vote a bit: __match_any_sync took
+// about 300 cycles for 64 experts.
+__device__ __forceinline__ unsigned lanes_with(int id, int bits) {
+    unsigned same = __ballot_sync(0xffffffffu, id >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = id >> b & 1;
+        const unsigned ones = __ballot_sync(0xffffffffu, one);
+        same &= one ? ones : ~ones;
+    }
+    return same;
 }
 
 // Slots of each expert in each block's tile.
@@ -52,11 +70,14 @@ __global__ void __launch_bounds__(kOrderThreads) order_count_kernel(const int32_
     for (int e = threadIdx.x; e < experts; e += blockDim.x) counts[(int64_t)blockIdx.x * experts + e] = hist[e];
 }
 
+// Bound by latency, not bytes: 32 tokens of four choices 3.1 us as one block; with the counting kernel 1024 of four
+// 6.1 us (as one block 11.3), 8192 of two 8.1 us (tiles of 2048 slots 10.8), 262144 of eight 47 us.
+//
 // A stable counting sort: a slot's row is the number of slots of lower experts, plus those of its own
 // expert in earlier blocks (from the counts), in earlier warps of this block, and earlier in its own
 // warp.  Each warp owns a contiguous run of the block's slots and its own counts, so nothing depends on
 // the order in which warps run.
-__global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* ids, int64_t n, int64_t tile, int experts,
+__global__ void __launch_bounds__(1024) order_kernel(const int32_t* ids, int64_t n, int64_t tile, int experts,
                                                               const int32_t* counts, int32_t* offsets, int32_t* row_of,
                                                               int32_t* slot_of) {
     extern __shared__ int32_t smem[];
@@ -70,24 +91,18 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* ids
     const int64_t per = ((tile + warps - 1) / warps + 31) / 32 * 32;
     const int64_t w0 = begin + warp * per, w1 = min(end, w0 + per);
     int32_t* mine = hist + warp * experts;
+    const int bits = 32 - __clz(experts - 1);
     for (int64_t i = w0; i < w1; i += 32) {
         const int id = load_id(ids, i + lane, w1, experts);
-        const unsigned same = __match_any_sync(0xffffffffu, id);
+        const unsigned same = lanes_with(id, bits);
         if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
         __syncwarp();
     }
     __syncthreads();
     // per expert: the counts of this block's warps become the rows before each warp's
     for (int e = threadIdx.x; e < experts; e += blockDim.x) {
-        int32_t here = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int32_t c = hist[w * experts + e];
-            hist[w * experts + e] = here;
-            here += c;
-        }
-        int32_t before = 0, all = here;
+        int32_t before = 0, all = 0;
         if (gridDim.x > 1) {
-            all = 0;
 #pragma unroll 8
             for (int b = 0; b < (int)gridDim.x; ++b) {
                 const int32_t c = counts[(int64_t)b * experts + e];
@@ -95,8 +110,17 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* ids
                 before += b < (int)blockIdx.x ? c : 0;
             }
         }
-        total[e] = all;
-        for (int w = 0; w < warps; ++w) hist[w * experts + e] += before;
+        for (int w = 0; w < warps; w += 4) {
+            int32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = hist[(w + i) * experts + e];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hist[(w + i) * experts + e] = before;
+                before += c[i];
+            }
+        }
+        total[e] = gridDim.x > 1 ? all : before;
     }
     __syncthreads();
     // exclusive scan of the totals over the experts: each thread scans a run of them
@@ -126,7 +150,7 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* ids
     __syncthreads();
     for (int64_t i = w0; i < w1; i += 32) {
         const int id = load_id(ids, i + lane, w1, experts);
-        const unsigned same = __match_any_sync(0xffffffffu, id);
+        const unsigned same = lanes_with(id, bits);
         int32_t row = -1;
         if (id >= 0) row = total[id] + mine[id] + __popc(same & ((1u << lane) - 1u));
         __syncwarp();
@@ -144,6 +168,7 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* ids
 
 // ------------------------------------------------------------------ rows
 constexpr int kRowThreads = 256;
+constexpr int32_t kMaxRowValues = 1 << 30;
 
 // The row of slot i, or -1: a dropped slot, or a row outside the buffer (reported).
 __device__ __forceinline__ int load_row(const int32_t* row_of, int64_t i, int32_t rows) {
@@ -212,7 +237,8 @@ __device__ __forceinline__ void store_vals(T* p, const float (&f)[V]) {
     }
 }
 
-// y[t] = add[t] + sum_j w[t][j] ys[row_of[t][j]], summed in fp32 in the order of j and rounded once.
+// y[t] = add[t] + sum_j w[t][j] ys[row_of[t][j]], summed in fp32 in the order of j and rounded once.  Bound by DRAM: 4096
+// tokens of four rows of 4096 bf16 33 us, 5.1 TB/s (floor 25.6); at an odd row length 54 us.
 // Without weights every w is 1 (the gather's gradient).  A thread takes E units of V values, kRowThreads units apart: V = 8
 // where every row starts on 16 bytes and d is a multiple of 8, with E = 1; else V = 1, with E = 8, so that it has as
 // many bytes in flight.
@@ -305,6 +331,7 @@ sgmv_status check_rows(const char* who, int32_t T, int32_t k, int32_t d, int32_t
     const std::string w(who);
     if (T < 0 || d < 1 || rows < 0) return fail(SGMV_ERR_INVALID, w + ": T, rows >= 0 and d >= 1 are required");
     if (k < 1 || k > kMaxExpertsPerToken) return fail(SGMV_ERR_INVALID, w + ": k must be in 1..64");
+    if (d > kMaxRowValues) return fail(SGMV_ERR_UNSUPPORTED, w + ": d must be at most 2^30");     // column numbers stay in 32 bits
     if ((int64_t)T * k > kMaxSlots) return fail(SGMV_ERR_UNSUPPORTED, w + ": T * k must be at most 2^30");
     if (T > 0 && (!row_of || !aligned(row_of, 4)))
         return fail(SGMV_ERR_INVALID, w + ": row_of is required, 4-byte aligned");
@@ -426,11 +453,12 @@ extern "C" sgmv_status sgmv_expert_order(const int32_t* expert_ids, int32_t T, i
     if (!offsets || !aligned(offsets, 4) ||
         (n > 0 && (!expert_ids || !row_of || !slot_of || !aligned(expert_ids, 4) || !aligned(row_of, 4) || !aligned(slot_of, 4))))
         return fail(SGMV_ERR_INVALID, "expert_order: expert_ids, offsets, row_of and slot_of are required, 4-byte aligned");
-    const int blocks = order_blocks(n, n_experts), warps = order_warps(n_experts);
+    const int blocks = order_blocks(n, n_experts);
     if (blocks > 1 && (!workspace || !aligned(workspace, 4))) return fail(SGMV_ERR_INVALID, "expert_order: a workspace is required, 4-byte aligned");
     if (blocks > 1 && workspace_bytes < (int64_t)blocks * n_experts * 4)
         return fail(SGMV_ERR_CAPACITY, "expert_order: the workspace is smaller than sgmv_expert_order_workspace says");
     const int64_t tile = (n + blocks - 1) / blocks;
+    const int warps = order_warps(tile, n_experts);
     int32_t* counts = static_cast<int32_t*>(workspace);
     const int smem = (warps * n_experts + n_experts + warps + 1) * 4;
     if (smem > 48 * 1024)

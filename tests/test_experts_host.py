@@ -153,3 +153,12 @@ def test_binding_refuses_shapes_and_types():
     with pytest.raises(sg.SgmvError):
         sg.expert_order(row_of, 0)
     sg.check_errors()
+
+
+def test_row_operators_refuse_rows_past_2_30_values():
+    """Column numbers are 32 bits wide."""
+    lib, d = sg.load_library(), (1 << 30) + 8
+    assert lib.sgmv_expert_gather(P, d, 1, d, 0, P, 1, P, d, 1, None) == 2
+    assert lib.sgmv_expert_gather_backward(P, d, 1, 1, d, 0, P, 1, P, d, None) == 2
+    assert lib.sgmv_expert_combine(P, d, 1, 0, P, None, 1, 1, d, None, 0, P, d, 0, None) == 2
+    assert lib.sgmv_expert_combine_backward(P, d, 0, P, d, 1, 0, P, None, 1, 1, d, P, d, P, None) == 2
