@@ -14,13 +14,20 @@ namespace {
 
 // Rows of a matrix, on average.
 int64_t rows_each(int64_t rows, int64_t experts) { return (rows + experts - 1) / experts; }
-// From this many rows a matrix on, the bf16 kernel is the faster: the integer kernel's epilogue grows with the rows and
-// with more of them a matrix it would read the codes again.  8192 x 8192, groups of 128: 16 rows 19.5 us by the integer
-// kernel, 24 rows 19.1 us by the bf16 kernel; one row 14.8 and 18.8 us.
-constexpr int kTcFrom = 17;
+// The integer kernel takes up to eight rows a matrix, its tile; experts average fewer than eight, since some then have
+// more, whose matrices it reads again.  Beyond, the bf16 kernel is the faster (us, integer and bf16 kernel):
+//   8192 x 8192, groups of 128:    1 row 14.8, 17.8;  8 rows 17.4, 18.3;  12 rows 18.8, 18.3
+//   28672 x 8192, groups of 64:    4 rows 46, 79;     8 rows 61, 79;      12 rows 86, 79
+//   14336 x 4096, groups of 32:    4 rows 24, 32;     8 rows 31, 32;      12 rows 44, 33
+//   16 experts of 2048 x 4096 with four rows each on average: groups of 32 64, 68, of 128 32, 39; with eight: 93, 69 and
+//   39, 39
+bool few_rows(int64_t rows, int64_t experts) {
+    const int64_t per = rows_each(rows, experts);
+    return experts == 1 ? per <= 8 : per < 8;
+}
 
 int64_t workspace_bytes(int64_t rows, int64_t experts, int64_t d_in, int64_t group, bool slots) {
-    if (rows_each(rows, experts) < kTcFrom) return base_i8_workspace(rows, d_in, group);
+    if (few_rows(rows, experts)) return base_i8_workspace(rows, d_in, group);
     return slots ? rows * d_in * 2 : 0;
 }
 
@@ -38,7 +45,7 @@ __global__ void __launch_bounds__(256) base_gather_kernel(BaseArgs a, uint4* to)
 
 cudaError_t launch_product(BaseArgs a, bool scale_f32, bool y_f32, void* workspace, cudaStream_t stream) {
     const int64_t per = rows_each(a.rows, a.experts);
-    if (per < kTcFrom) return launch_base_i8(a, per, scale_f32, y_f32, workspace, stream);
+    if (few_rows(a.rows, a.experts)) return launch_base_i8(a, per, scale_f32, y_f32, workspace, stream);
     if (a.slot_of) {
         base_gather_kernel<<<a.rows, 256, 0, stream>>>(a, static_cast<uint4*>(workspace));
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;

@@ -26,7 +26,8 @@ namespace {
 // The digits' K order inside eight values is 0 2 4 6 1 3 5 7: the even and the odd nibbles of a word of codes are two
 // words of bytes.  The codes go to tensor memory as the A operand (a thread a row, a lane a row); digit d of row t is
 // row 4 t + d of B, so that a row's sums are four neighbouring columns (the last one unused).  Two lanes (MMA warp,
-// accumulators, epilogue warps) take alternate groups, or pairs of groups where there is room for four accumulators.
+// accumulators, epilogue warps) take alternate pairs of groups, or
+// fours where there is room for eight accumulators.
 // K is split over the CTAs of a cluster; two CTAs share an SM.
 //
 // What bounds it: 8192 x 8192, groups of 128, one row: 14.8 us with the first kernel (floor 5.3).  Of the 13 us on the
@@ -42,8 +43,8 @@ struct I8Config {
     static constexpr int kThreads = (4 + kConvert + kEpilogue) * 32;
     static constexpr int kRegisters = 64;                            // a thread at launch
     static constexpr int kCols = 4 * TT;                             // columns of an MMA
-    static constexpr int kBatch = TT == 4 && G < 128 ? 4 : TT <= 8 ? 2 : 1;      // groups that a lane hands over together
-    static constexpr int kLoad = kBatch < 2 ? kBatch : 2;            // of them, in registers at a time
+    static constexpr int kBatch = TT == 4 && G < 128 ? 4 : 2;      // groups that a lane hands over together
+    static constexpr int kLoad = 2;                                  // of them, in registers at a time
     static constexpr int kStages = 4;                                // of 128 K values
     static constexpr int kCodeStages = 3;                            // of 256 K values
     static constexpr int kB = kCols * 128, kCodes = 128 * 128;
@@ -481,7 +482,7 @@ cudaError_t launch_g(const BaseArgs& a, int64_t per, const Digits& in, bool scal
     // eight-row kernel's two groups 46).  Experts of two rows on average and groups of 128, whose batches are two here
     // too, only lose by units of four rows: 56.8 against 55.6 us for 64 experts of 1536 x 4096.
     if (per <= 4 && (G < 128 || !a.offsets)) return launch_t<G, 4, Z>(a, in, scale_f32, y_f32, stream);
-    return per <= 8 ? launch_t<G, 8, Z>(a, in, scale_f32, y_f32, stream) : launch_t<G, 16, Z>(a, in, scale_f32, y_f32, stream);
+    return launch_t<G, 8, Z>(a, in, scale_f32, y_f32, stream);
 }
 
 }  // namespace

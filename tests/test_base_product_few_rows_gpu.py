@@ -1,4 +1,4 @@
-"""Base products of up to 16 rows a matrix, whose x is held in fixed point of 256 values each.
+"""Base products of few rows a matrix: of up to 8, x is held in fixed point of 256 values each.
 
 Bounds: with m the largest magnitude of x in a block of 256 values and 2^E <= m < 2^(E+1), a value of the block is off by
 at most half a unit, 2^(E-22) <= 2^-22 m, and not at all if its magnitude is 2^(E-14) or more.  So an output is off by

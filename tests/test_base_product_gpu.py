@@ -2,7 +2,7 @@
 
 Exact cases: x of small integers and scales that are powers of two make every partial sum a multiple of 2^-3
 below 2^20, so that fp32 sums in any order are exact and y has to be the rounded 64-bit value bit for bit.
-Real-valued cases (with fewer than 17 rows also tests/test_base_product_few_rows_gpu.py): with S = sum |s (q - z) x| of an output, each of fewer than 2 d_in additions and scalings in
+Real-valued cases (of up to 8 rows also tests/test_base_product_few_rows_gpu.py): with S = sum |s (q - z) x| of an output, each of fewer than 2 d_in additions and scalings in
 fp32 is off by at most 2^-23 of a partial result no larger than S (a tensor core may truncate where an fma
 rounds), so |y - y64| <= 2 d_in 2^-23 S, plus half a step of y's type."""
 import numpy as np

@@ -50,7 +50,7 @@ def experts(**kw):
 def test_base_product_experts_workspace():
     lib = sg.load_library()
     f = lib.sgmv_base_product_experts_workspace
-    assert f(16, 64, 64, 1, 0) == f(16, 64, 64, 1, 1) == lib.sgmv_base_product_workspace(16, 64, 64) and f(0, 64, 64, 3, 1) == 0
+    assert f(8, 64, 64, 1, 0) == f(8, 64, 64, 1, 1) == lib.sgmv_base_product_workspace(8, 64, 64) > 0 and f(0, 64, 64, 3, 1) == 0
     assert f(17, 64, 64, 1, 0) == 0 and f(17, 64, 64, 1, 1) == 17 * 128
     assert f(-1, 64, 64, 1, 0) == f(1, 64, 64, 4097, 0) == f(1, 64, 64, 0, 0) == f(1, 64, 16, 1, 0) == -1
     many = dict(rows=400, x_rows=400, slot_of=P)
