@@ -743,17 +743,21 @@ def _workspace(need: int, like: torch.Tensor, stream) -> Optional[int]:
 def _weights4(codes, scales, zeros, lead: int, device: int):
     """Checks and addresses of a 4-bit matrix: codes [.., d_out, d_in / 2], scales and zeros [.., d_out, d_in / group]."""
     pc = _flat(codes, "codes", torch.uint8, device)
-    _need(codes.dim() == 2 + lead and scales.dim() == 2 + lead and scales.shape[:-1] == codes.shape[:-1],
-          "codes and scales must have the same leading dimensions")
-    _need(scales.dtype in _DTYPE, "scales must be bf16 or fp32")
-    ps = _flat(scales, "scales", scales.dtype, device)
-    d_in, n_groups = 2 * codes.shape[-1], scales.shape[-1]
-    _need(n_groups > 0 and d_in % n_groups == 0, "d_in must be a multiple of the number of groups")
+    cs, ss, sdt = codes.shape, scales.shape, scales.dtype
+    if len(cs) != 2 + lead or len(ss) != 2 + lead or ss[0] != cs[0] or ss[lead] != cs[lead]:
+        raise ValueError("codes and scales must have the same leading dimensions")
+    if sdt not in _DTYPE:
+        raise ValueError("scales must be bf16 or fp32")
+    ps = _flat(scales, "scales", sdt, device)
+    d_in, n_groups = 2 * cs[-1], ss[-1]
+    if n_groups <= 0 or d_in % n_groups:
+        raise ValueError("d_in must be a multiple of the number of groups")
     pz = None
     if zeros is not None:
         pz = _flat(zeros, "zeros", torch.uint8, device)
-        _need(zeros.shape == scales.shape, "zeros must have the shape of scales")
-    return pc, ps, _DTYPE[scales.dtype], pz, d_in, d_in // n_groups
+        if zeros.shape != ss:
+            raise ValueError("zeros must have the shape of scales")
+    return pc, ps, _DTYPE[sdt], pz, d_in, d_in // n_groups
 
 
 def base_product(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor, zeros=None,
@@ -766,9 +770,11 @@ def base_product(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, y: 
     pc, ps, sdt, pz, d_in, group = _weights4(codes, scales, zeros, 0, dev)
     px, ldx = _mat(x, "x", dev)
     py, ldy = _mat(y, "y", dev)
-    T, d_out = x.shape[0], codes.shape[0]
-    _need(x.dtype == torch.bfloat16 and x.shape[1] == d_in, "x must be bf16 [T, d_in]")
-    _need(y.shape[0] == T and y.shape[1] == d_out, "y must be [T, d_out]")
+    (T, width), (rows, d_out) = x.shape, y.shape
+    if x.dtype is not torch.bfloat16 or width != d_in:
+        raise ValueError("x must be bf16 [T, d_in]")
+    if rows != T or d_out != codes.shape[0]:
+        raise ValueError("y must be [T, d_out]")
     lib = _lib or load_library()
     need = lib.sgmv_base_product_workspace(T, d_in, group)
     pw = _workspace(need, x, stream)
